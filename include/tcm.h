@@ -86,6 +86,25 @@ enum { TCM_F16_F32 = 0, TCM_BF16_F32 = 1, TCM_F32_F32 = 2, TCM_I8_I32 = 3 };
 #define TCM_C_F16 (1 << 10)
 #define TCM_C_BF16 (1 << 11)
 
+/* ---- 8-bit floating types ------------------------------------------------- */
+/*   TCM_E4M3_F32 : tcm_gemm_fp8's element type: A and B 8-bit floats, e4m3
+ *                  (4 exponent bits, largest value 448, no infinities) or by
+ *                  the two flags e5m2 (largest 57344), with binary32 scales;
+ *                  accumulate and C in binary32; bias f32                   */
+enum { TCM_E4M3_F32 = 4 };
+/* flags of tcm_gemm_fp8 */
+#define TCM_A_E5M2 (1 << 12)
+#define TCM_B_E5M2 (1 << 13)
+#define TCM_B_ROW_SCALES (1 << 14) /* B's scales cover 1 x 128 blocks, not 128 x 128 tiles */
+/* flags of tcm_quantize_fp8 */
+#define TCM_Q_E5M2 (1 << 15)     /* e5m2 outputs, not e4m3 */
+#define TCM_BLOCK_TILE (1 << 16) /* a scale for each 128 x 128 tile, not for each 1 x 128 block */
+/* flags of tcm_moe_route */
+#define TCM_ROUTE_SIGMOID (1 << 17) /* scores are sigmoids, not a softmax */
+#define TCM_ROUTE_NORM (1 << 18)    /* a token's weights sum to `scale` */
+/* flag of tcm_moe */
+#define TCM_W_E4M3 (1 << 19) /* expert weights in e4m3 with tile scales, not in x's type */
+
 /* ---- epilogue flags -------------------------------------------------------- */
 /* TCM_EPI_BIAS:  bias[j] (length N, f32 or int32 per dtype) seeds the
  *                accumulator of column j before any product is added.
@@ -291,6 +310,134 @@ int tcm_conv2d(int64_t N, int64_t H, int64_t W, int64_t C, int64_t K, int64_t R,
                int64_t dil_h, int64_t dil_w,
                const void* x, const void* f, void* y,
                int dtype, const void* bias, int epilogue, void* stream);
+
+/*
+ * tcm_quantize_fp8 -- a matrix to 8-bit floats with one binary32 scale for
+ * each block of 128 of its values (the mixed precision of the Tensor Core
+ * notes, je-d.tistory.com/entry/tvm, one step narrower: operands in 8 bits
+ * need a range of their own for each block):
+ *
+ *     s = max(amax |x| / L, 2^-126),   q = nearest value to x / s (ties to even),
+ *
+ * L = 448 for e4m3, 57344 with TCM_Q_E5M2.  q is the nearest value to the
+ * exact quotient.  X is rows x cols, row-major, ldx >= cols, of the type in
+ * `dtype` (TCM_F16_F32, TCM_BF16_F32 or TCM_F32_F32).  Two outputs, either of
+ * which may be NULL (not both), from one read of X:
+ *
+ *   Q, S     X as it lies: Q[r*ldq + c], ldq >= cols.  Blocks are 128
+ *            consecutive columns of a row: S[(c/128)*lds + r], lds >= rows; or
+ *            with TCM_BLOCK_TILE 128 x 128 tiles: S[(r/128)*lds + c/128],
+ *            lds >= ceil(cols/128).
+ *   QT, ST   X transposed: QT[c*ldqt + r], ldqt >= rows.  Blocks are 128
+ *            consecutive rows of a column: ST[(r/128)*ldst + c], ldst >= cols;
+ *            or tiles: ST[(c/128)*ldst + r/128], ldst >= ceil(rows/128).
+ *
+ * (Q, S) and (QT, ST) are operands of tcm_gemm_fp8 as they come: a layer's
+ * input gives the forward product's A and, transposed, the weight gradient's
+ * B; tiles of a weight serve the forward product and, transposed, the input
+ * gradient.  Blocks at an edge hold what is left; bytes past a row's end are
+ * not written.  A block with a NaN gets a NaN scale and NaN values; one with
+ * an infinity an infinite scale, zeros, and NaN for the infinities.  Any
+ * alignment and leading dimension of X, Q and QT; S and ST 4-byte aligned.
+ * Outputs must not overlap X or each other.  rows or cols 0: nothing to do.
+ * Returns TCM_OK once enqueued; TCM_ERR_INVALID_VALUE; TCM_ERR_HIP.
+ * Allocates nothing.
+ */
+int tcm_quantize_fp8(int64_t rows, int64_t cols, const void* X, int64_t ldx, int dtype,
+                     void* Q, int64_t ldq, float* S, int64_t lds,
+                     void* QT, int64_t ldqt, float* ST, int64_t ldst, void* stream);
+
+/*
+ * tcm_gemm_fp8 -- the product of two matrices in 8-bit floating point with a
+ * scale for each block of 128 along k,
+ *
+ *     C[m][n] = epi( [C_in[m][n] +] bias[n] +
+ *                    sum_b sa[b][m] * sb[b, n] * sum_{k in block b} A[m][k] * B[n][k] ).
+ *
+ * A block's products are summed in binary32 on the matrix cores, multiplied
+ * by its two scales and added to a binary32 accumulator.
+ *
+ *   M, N, K      sizes, 0 <= size < 2^31; empty and K == 0 as tcm_gemm.
+ *   A, lda       M x K, k contiguous, lda >= K; e4m3 or, with TCM_A_E5M2, e5m2.
+ *   SA, ldsa     A's scales, [ceil(K/128)][ldsa], ldsa >= M.
+ *   B, ldb       N x K, k contiguous, ldb >= K; e4m3 or, with TCM_B_E5M2, e5m2.
+ *   SB, ldsb     B's scales: one for each 128 x 128 tile, SB[(n/128)*ldsb + k/128],
+ *                ldsb >= ceil(K/128); or with TCM_B_ROW_SCALES one for each
+ *                1 x 128 block, SB[(k/128)*ldsb + n], ldsb >= N.
+ *   C, ldc       M x N row-major, ldc >= N; f32, or by TCM_C_F16 / TCM_C_BF16
+ *                rounded to nearest even.  Must not overlap an input.
+ *   dtype        TCM_E4M3_F32, or-ed with the flags named here.
+ *   bias, epilogue, stream   as tcm_gemm (all of TCM_EPI_*; bias is float).
+ *
+ * A training step's three products are this one: y = x W^T + bias (A = x in
+ * row blocks, B = W in tiles), dx = dy W (A = dy, B = W transposed), dW =
+ * dy^T x (both operands transposed, TCM_B_ROW_SCALES, TCM_EPI_ACCUM to add to
+ * a gradient).  Any alignment and leading dimension is served; the fast
+ * kernels take A, B and C 16-byte aligned with lda and ldb multiples of 16.
+ * SA, SB and bias are 4-byte aligned.  K needs no alignment: bytes between K
+ * and the leading dimension are never used.
+ * Returns as tcm_gemm; the workspace rules are tcm_gemm's.
+ */
+int tcm_gemm_fp8(int64_t M, int64_t N, int64_t K,
+                 const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                 const void* B, int64_t ldb, const float* SB, int64_t ldsb,
+                 void* C, int64_t ldc, int dtype, const float* bias, int epilogue,
+                 void* stream);
+
+/*
+ * tcm_moe_route -- the experts of every token and the weights of their
+ * outputs:
+ *
+ *     score = softmax(x) over the experts, or with TCM_ROUTE_SIGMOID 1 / (1 + exp(-x)),
+ *     key   = score + bias[expert], or without a bias x itself,
+ *     ids   = the topk experts of the largest keys, largest first, ties to
+ *             the lower expert,
+ *     weight = scale * score[id], with TCM_ROUTE_NORM divided by the sum of
+ *             the chosen scores.
+ *
+ *   logits, ldx  tokens x experts, ldx >= experts, of the type in `dtype`
+ *                (TCM_F16_F32, TCM_BF16_F32 or TCM_F32_F32; any alignment).
+ *   bias         `experts` floats or NULL: moves the choice, not the weights
+ *                (the bias that balances the experts' load).
+ *   ids, weights tokens x topk, dense; must not overlap an input.
+ * experts <= 1024 and topk <= 64 (else TCM_ERR_NOT_SUPPORTED), topk <=
+ * experts.  Keys with a bias are formed in binary64.  A NaN key ranks above
+ * every number; a sum of zero (a row of -inf) gives weights of zero; a
+ * softmax over NaN or +inf is NaN.  Returns as tcm_quantize_fp8.
+ */
+int tcm_moe_route(int64_t tokens, int64_t experts, int64_t topk,
+                  const void* logits, int64_t ldx, int dtype,
+                  const float* bias, float scale,
+                  int32_t* ids, float* weights, void* stream);
+
+/*
+ * tcm_moe -- a whole mixture-of-experts layer, made for a few tokens (a
+ * decoding batch, where every product is bound by reading the chosen experts'
+ * weights once):
+ *
+ *     out[t] = sum over slots j of weights[t][j] * W2_e ( silu(W1_e,gate x[t]) * (W1_e,up x[t]) ),
+ *     e = ids[t][j],   silu(g) = g / (1 + exp(-g)).
+ *
+ *   X, ldx       tokens x hidden, f16 or bf16 by `dtype`, ldx >= hidden.
+ *   ids, weights tokens x topk, dense (tcm_moe_route's).  An id outside
+ *                [0, experts) adds nothing; an id may repeat.
+ *   W1           [experts][2][inter][hidden] dense, gate rows then up rows, in
+ *                x's type or with TCM_W_E4M3 in e4m3 with tile scales
+ *   S1           [experts][2][ceil(inter/128)][ceil(hidden/128)] (else NULL).
+ *   W2, S2       [experts][hidden][inter], [experts][ceil(hidden/128)][ceil(inter/128)].
+ *   out, ldo     tokens x hidden of x's type, ldo >= hidden; written whole;
+ *                must not overlap an input.
+ *   dtype        TCM_F16_F32 | TCM_C_F16 or TCM_BF16_F32 | TCM_C_BF16,
+ *                optionally | TCM_W_E4M3.
+ * Sums are binary32; the products between the two matrices stay in binary32
+ * or in two 16-bit parts that hold it to 16 bits or more.  Any alignment of
+ * X, W1, W2 and out; ids, weights and scales 4-byte aligned.  Returns as
+ * tcm_gemm; the workspace rules are tcm_gemm's.
+ */
+int tcm_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t topk,
+            const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+            const void* W1, const float* S1, const void* W2, const float* S2,
+            void* out, int64_t ldo, int dtype, void* stream);
 
 /* Text of a status code (static storage; never NULL). */
 const char* tcm_status_string(int status);

@@ -19,6 +19,11 @@ LIB_PATH = os.path.join(HERE, "_build", "libtcm.so")
 TCM_F16_F32, TCM_BF16_F32, TCM_F32_F32, TCM_I8_I32 = 0, 1, 2, 3
 TCM_A_COLMAJOR, TCM_B_COLMAJOR = 1 << 8, 1 << 9
 TCM_C_F16, TCM_C_BF16 = 1 << 10, 1 << 11
+TCM_E4M3_F32 = 4
+TCM_A_E5M2, TCM_B_E5M2, TCM_B_ROW_SCALES = 1 << 12, 1 << 13, 1 << 14
+TCM_Q_E5M2, TCM_BLOCK_TILE = 1 << 15, 1 << 16
+TCM_ROUTE_SIGMOID, TCM_ROUTE_NORM = 1 << 17, 1 << 18
+TCM_W_E4M3 = 1 << 19
 TCM_EPI_NONE, TCM_EPI_BIAS, TCM_EPI_RELU, TCM_EPI_BIAS_RELU, TCM_EPI_ACCUM = 0, 1, 2, 3, 4
 TCM_OK, TCM_ERR_INVALID_VALUE, TCM_ERR_NOT_SUPPORTED, TCM_ERR_HIP, TCM_ERR_ALLOC = 0, 1, 2, 3, 4
 TCM_MAX_GROUP = 32
@@ -69,6 +74,14 @@ def lib():
         L.tcm_gemm_grouped.restype = ci
         L.tcm_conv2d.argtypes = [i64] * 13 + [vp, vp, vp, ci, vp, ci, vp]
         L.tcm_conv2d.restype = ci
+        L.tcm_quantize_fp8.argtypes = [i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.tcm_quantize_fp8.restype = ci
+        L.tcm_gemm_fp8.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, ci, vp]
+        L.tcm_gemm_fp8.restype = ci
+        L.tcm_moe_route.argtypes = [i64, i64, i64, vp, i64, ci, vp, ctypes.c_float, vp, vp, vp]
+        L.tcm_moe_route.restype = ci
+        L.tcm_moe.argtypes = [i64] * 5 + [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci, vp]
+        L.tcm_moe.restype = ci
         L.tcm_status_string.argtypes = [ci]
         L.tcm_status_string.restype = ctypes.c_char_p
         L.tcm_set_option.argtypes = [ctypes.c_char_p, i64]
@@ -236,6 +249,30 @@ def tcm_conv2d(N, H, W, C, K, R, S, pad_h, pad_w, stride_h, stride_w, dil_h, dil
     addresses as ints).  Returns the tcm status code."""
     return lib().tcm_conv2d(N, H, W, C, K, R, S, pad_h, pad_w, stride_h, stride_w, dil_h, dil_w, x, f, y, dtype, bias,
                             epilogue, stream)
+
+
+def tcm_quantize_fp8(rows, cols, X, ldx, dtype, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream):
+    """X in 8-bit floats with a scale a block, as it lies (Q, S) and/or
+    transposed (QT, ST).  Returns the tcm status code."""
+    return lib().tcm_quantize_fp8(rows, cols, X, ldx, dtype, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream)
+
+
+def tcm_gemm_fp8(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, dtype, bias, epilogue, stream):
+    """C = epi(bias + A.B^T) of 8-bit operands with block scales.  Returns
+    the tcm status code."""
+    return lib().tcm_gemm_fp8(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, dtype, bias, epilogue, stream)
+
+
+def tcm_moe_route(tokens, experts, topk, logits, ldx, dtype, bias, scale, ids, weights, stream):
+    """Every token's topk experts and their weights.  Returns the tcm status
+    code."""
+    return lib().tcm_moe_route(tokens, experts, topk, logits, ldx, dtype, bias, scale, ids, weights, stream)
+
+
+def tcm_moe(tokens, hidden, inter, experts, topk, X, ldx, ids, weights, W1, S1, W2, S2, out, ldo, dtype, stream):
+    """A mixture-of-experts layer for a few tokens.  Returns the tcm status
+    code."""
+    return lib().tcm_moe(tokens, hidden, inter, experts, topk, X, ldx, ids, weights, W1, S1, W2, S2, out, ldo, dtype, stream)
 
 
 def tcm_version():

@@ -1,0 +1,82 @@
+// Arguments and launchers of the block-scaled 8-bit product, its quantiser,
+// the expert router and the mixture-of-experts layer (tcm_gemm_fp8,
+// tcm_quantize_fp8, tcm_moe_route, tcm_moe), shared by the C ABI and the
+// kernels.
+#pragma once
+#include <cstdint>
+
+namespace tcm {
+
+// One scale covers kScaleBlock values of a row, or a kScaleBlock-square tile.
+constexpr int kScaleBlock = 128;
+constexpr int64_t scale_blocks(int64_t n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+// The largest values of the two 8-bit formats, and the least scale: a block
+// of zeros keeps a normal, finite one.
+constexpr float kE4M3Max = 448.f, kE5M2Max = 57344.f;
+constexpr float kScaleMin = 0x1p-126f;
+
+struct QuantArgs {
+    const void* x;
+    int64_t rows, cols, ldx;
+    unsigned char* q;      // [rows][cols] as x lies, or null
+    int64_t ldq;
+    float* s;              // its scales
+    int64_t lds;
+    unsigned char* qt;     // [cols][rows], or null
+    int64_t ldqt;
+    float* st;
+    int64_t ldst;
+};
+// x_type: F16, BF16 or F32
+int launch_quantize(int x_type, bool e5m2, bool tile, const QuantArgs& a, void* stream);
+
+struct Fp8Args {
+    const unsigned char* A;  // [M][K]
+    const unsigned char* B;  // [N][K]
+    void* C;                 // [M][N]
+    const float* sa;         // [k block][row of A]
+    const float* sb;         // [row tile of B][k block], or with b_row [k block][row of B]
+    const float* bias;
+    int64_t M, N, K, lda, ldb, ldc, ldsa, ldsb;
+    int a_e5m2, b_e5m2, b_row;
+    int has_bias, relu, accum, c_type;
+};
+// any alignment, leading dimension and size
+int launch_fp8_generic(const Fp8Args& a, void* stream);
+
+struct RouteArgs {
+    const void* x;         // [tokens][experts]
+    int64_t tokens, ldx;
+    int experts, topk;
+    int sigmoid, norm;
+    const float* bias;     // [experts], added to the scores for the choice only, or null
+    float scale;
+    int* ids;              // [tokens][topk]
+    float* weights;        // [tokens][topk]
+};
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTopk = 64;
+int launch_route(int x_type, const RouteArgs& a, void* stream);
+
+struct MoeArgs {
+    const void* x;         // [tokens][hidden], 16-bit
+    int64_t ldx;
+    const int* ids;        // [tokens][topk]
+    const float* weights;
+    const void* w1;        // [experts][gate, up][inter][hidden]
+    const float* s1;       // [experts][gate, up][inter tile][hidden tile] (8-bit weights)
+    const void* w2;        // [experts][hidden][inter]
+    const float* s2;
+    void* out;             // [tokens][hidden], x's type
+    int64_t ldo;
+    int tokens, hidden, inter, experts, topk;
+    void* ws;              // moe_workspace_bytes of scratch
+};
+int64_t moe_generic_workspace(const MoeArgs& a);
+int launch_moe_generic(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
+
+// Shared with the C ABI's other entry points (tcm_api.cpp): the stream's
+// workspace, grown to `bytes` (a tcm_status), and the text of tcm_last_plan.
+int workspace_for(void* stream, int64_t bytes, void** out);
+void set_last_plan(const char* text);
+
+}  // namespace tcm

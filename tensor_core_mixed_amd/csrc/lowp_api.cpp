@@ -1,0 +1,289 @@
+// C ABI of the block-scaled 8-bit product, its quantiser, the expert router
+// and the mixture-of-experts layer (declared in include/tcm.h): argument
+// checks and dispatch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdio>
+#include <exception>
+
+#include "../../include/tcm.h"
+#include "lowp.h"
+#include "tcm_internal.h"
+
+namespace tcm {
+namespace {
+
+constexpr int64_t kDim = (int64_t)1 << 31;
+
+// bytes of a rows x cols matrix of leading dimension ld; -1 past 2^62
+int64_t span_of(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+    if (rows == 0 || cols == 0) return 0;
+    if (rows > 1 && ld > (((int64_t)1 << 60) - cols) / (rows - 1)) return -1;
+    const int64_t n = (rows - 1) * ld + cols;
+    return n > ((int64_t)1 << 62) / es ? -1 : n * es;
+}
+
+struct Region {
+    const void* p;
+    int64_t bytes;
+};
+bool cross(const Region& a, const Region& b) {
+    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+    const char *x = (const char*)a.p, *y = (const char*)b.p;
+    return x < y + b.bytes && y < x + a.bytes;
+}
+// no output crosses another output or an input
+template <int NO, int NI>
+bool disjoint(const Region (&out)[NO], const Region (&in)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = i + 1; j < NO; ++j)
+            if (cross(out[i], out[j])) return false;
+        for (const Region& r : in)
+            if (cross(out[i], r)) return false;
+    }
+    return true;
+}
+bool word_aligned(const void* p) { return ((uintptr_t)p & 3) == 0; }
+
+int done(int hip_status) { return hip_status == 0 ? TCM_OK : TCM_ERR_HIP; }
+
+int quantize_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dtype, void* q, int64_t ldq, float* s,
+                  int64_t lds, void* qt, int64_t ldqt, float* st, int64_t ldst, void* stream) {
+    const int t = dtype & 0xff, flags = dtype & ~0xff;
+    if (t != F16 && t != BF16 && t != F32) return TCM_ERR_INVALID_VALUE;
+    if (flags & ~(TCM_Q_E5M2 | TCM_BLOCK_TILE)) return TCM_ERR_INVALID_VALUE;
+    const bool tile = flags & TCM_BLOCK_TILE;
+    if (rows < 0 || cols < 0 || rows >= kDim || cols >= kDim || ldx < std::max<int64_t>(cols, 1)) return TCM_ERR_INVALID_VALUE;
+    const int64_t rb = scale_blocks(rows), cb = scale_blocks(cols);
+    if (q && (ldq < std::max<int64_t>(cols, 1) || lds < std::max<int64_t>(tile ? cb : rows, 1))) return TCM_ERR_INVALID_VALUE;
+    if (qt && (ldqt < std::max<int64_t>(rows, 1) || ldst < std::max<int64_t>(tile ? rb : cols, 1))) return TCM_ERR_INVALID_VALUE;
+    if (rows == 0 || cols == 0) {
+        set_last_plan("empty problem");
+        return TCM_OK;
+    }
+    if (!x || (!q && !qt) || (q && !s) || (qt && !st)) return TCM_ERR_INVALID_VALUE;
+    if ((q && !word_aligned(s)) || (qt && !word_aligned(st))) return TCM_ERR_INVALID_VALUE;
+    const int64_t xb = span_of(rows, cols, ldx, elem_bytes(t));
+    const int64_t qb = q ? span_of(rows, cols, ldq, 1) : 0, qtb = qt ? span_of(cols, rows, ldqt, 1) : 0;
+    const int64_t sb = q ? (tile ? span_of(rb, cb, lds, 4) : span_of(cb, rows, lds, 4)) : 0;
+    const int64_t stb = qt ? (tile ? span_of(cb, rb, ldst, 4) : span_of(rb, cols, ldst, 4)) : 0;
+    if (xb < 0 || qb < 0 || qtb < 0 || sb < 0 || stb < 0) return TCM_ERR_INVALID_VALUE;
+    const Region out[4] = {{q, qb}, {qt, qtb}, {s, sb}, {st, stb}}, in[1] = {{x, xb}};
+    if (!disjoint(out, in)) return TCM_ERR_INVALID_VALUE;
+    QuantArgs a{};
+    a.x = x;
+    a.rows = rows;
+    a.cols = cols;
+    a.ldx = ldx;
+    a.q = (unsigned char*)q;
+    a.ldq = ldq;
+    a.s = s;
+    a.lds = lds;
+    a.qt = (unsigned char*)qt;
+    a.ldqt = ldqt;
+    a.st = st;
+    a.ldst = ldst;
+    char text[160];
+    snprintf(text, sizeof text, "kernel=quantize rows=%lld cols=%lld dtype=%d e5m2=%d block=%s out=%s", (long long)rows,
+             (long long)cols, t, (flags & TCM_Q_E5M2) != 0, tile ? "tile" : "row", q ? (qt ? "both" : "rows") : "cols");
+    set_last_plan(text);
+    return done(launch_quantize(t, flags & TCM_Q_E5M2, tile, a, stream));
+}
+
+int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* sa, int64_t ldsa, const void* B,
+                  int64_t ldb, const float* sb, int64_t ldsb, void* C, int64_t ldc, int dtype, const float* bias, int epilogue,
+                  void* stream) {
+    const int flags = dtype & ~0xff;
+    if ((dtype & 0xff) != TCM_E4M3_F32) return TCM_ERR_INVALID_VALUE;
+    if (flags & ~(TCM_A_E5M2 | TCM_B_E5M2 | TCM_B_ROW_SCALES | TCM_C_F16 | TCM_C_BF16)) return TCM_ERR_INVALID_VALUE;
+    if ((flags & TCM_C_F16) && (flags & TCM_C_BF16)) return TCM_ERR_INVALID_VALUE;
+    if (epilogue < 0 || epilogue > (TCM_EPI_BIAS | TCM_EPI_RELU | TCM_EPI_ACCUM)) return TCM_ERR_INVALID_VALUE;
+    if (M < 0 || N < 0 || K < 0 || M >= kDim || N >= kDim || K >= kDim) return TCM_ERR_INVALID_VALUE;
+    const bool b_row = flags & TCM_B_ROW_SCALES;
+    const int64_t kb = scale_blocks(K), nb = scale_blocks(N);
+    if (lda < std::max<int64_t>(K, 1) || ldb < std::max<int64_t>(K, 1) || ldc < std::max<int64_t>(N, 1)) return TCM_ERR_INVALID_VALUE;
+    if (ldsa < std::max<int64_t>(M, 1) || ldsb < std::max<int64_t>(b_row ? N : kb, 1)) return TCM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) {
+        set_last_plan("empty problem");
+        return TCM_OK;
+    }
+    const bool use_bias = epilogue & TCM_EPI_BIAS;
+    if (!C || (use_bias && !bias) || (K > 0 && (!A || !B || !sa || !sb))) return TCM_ERR_INVALID_VALUE;
+    if (!word_aligned(sa) || !word_aligned(sb) || (use_bias && !word_aligned(bias))) return TCM_ERR_INVALID_VALUE;
+    const int c_type = (flags & TCM_C_F16) ? C_F16 : ((flags & TCM_C_BF16) ? C_BF16 : C_ACC);
+    const int64_t ab = K ? span_of(M, K, lda, 1) : 0, bb = K ? span_of(N, K, ldb, 1) : 0;
+    const int64_t cb = span_of(M, N, ldc, c_elem_bytes(c_type));
+    const int64_t sab = span_of(kb, M, ldsa, 4), sbb = b_row ? span_of(kb, N, ldsb, 4) : span_of(nb, kb, ldsb, 4);
+    if (ab < 0 || bb < 0 || cb < 0 || sab < 0 || sbb < 0) return TCM_ERR_INVALID_VALUE;
+    const Region out[1] = {{C, cb}}, in[5] = {{A, ab}, {B, bb}, {sa, sab}, {sb, sbb}, {use_bias ? bias : nullptr, N * 4}};
+    if (!disjoint(out, in)) return TCM_ERR_INVALID_VALUE;
+    Fp8Args a{};
+    a.A = (const unsigned char*)A;
+    a.B = (const unsigned char*)B;
+    a.C = C;
+    a.sa = sa;
+    a.sb = sb;
+    a.bias = bias;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.ldsa = ldsa;
+    a.ldsb = ldsb;
+    a.a_e5m2 = (flags & TCM_A_E5M2) != 0;
+    a.b_e5m2 = (flags & TCM_B_E5M2) != 0;
+    a.b_row = b_row;
+    a.has_bias = use_bias;
+    a.relu = (epilogue & TCM_EPI_RELU) != 0;
+    a.accum = (epilogue & TCM_EPI_ACCUM) != 0;
+    a.c_type = c_type;
+    char text[160];
+    // (a launch counts its threads in 32 bits)
+    if (((M + 63) / 64) * ((N + 63) / 64) >= ((int64_t)1 << 24)) return TCM_ERR_NOT_SUPPORTED;
+    snprintf(text, sizeof text, "kernel=fp8_generic M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+    set_last_plan(text);
+    return done(launch_fp8_generic(a, stream));
+}
+
+int route_impl(int64_t tokens, int64_t experts, int64_t topk, const void* logits, int64_t ldx, int dtype, const float* bias,
+               float scale, int* ids, float* weights, void* stream) {
+    const int t = dtype & 0xff, flags = dtype & ~0xff;
+    if (t != F16 && t != BF16 && t != F32) return TCM_ERR_INVALID_VALUE;
+    if (flags & ~(TCM_ROUTE_SIGMOID | TCM_ROUTE_NORM)) return TCM_ERR_INVALID_VALUE;
+    if (tokens < 0 || experts < 0 || topk < 0 || tokens >= ((int64_t)1 << 40) || topk > experts) return TCM_ERR_INVALID_VALUE;
+    if (ldx < std::max<int64_t>(experts, 1)) return TCM_ERR_INVALID_VALUE;
+    if (experts > kRouteMaxExperts || topk > kRouteMaxTopk) return TCM_ERR_NOT_SUPPORTED;
+    if (tokens == 0 || topk == 0) {
+        set_last_plan("empty problem");
+        return TCM_OK;
+    }
+    if (!logits || !ids || !weights) return TCM_ERR_INVALID_VALUE;
+    if (!word_aligned(ids) || !word_aligned(weights) || (bias && !word_aligned(bias))) return TCM_ERR_INVALID_VALUE;
+    const int64_t xb = span_of(tokens, experts, ldx, elem_bytes(t));
+    if (xb < 0) return TCM_ERR_INVALID_VALUE;
+    const Region out[2] = {{ids, tokens * topk * 4}, {weights, tokens * topk * 4}}, in[2] = {{logits, xb}, {bias, experts * 4}};
+    if (!disjoint(out, in)) return TCM_ERR_INVALID_VALUE;
+    RouteArgs a{};
+    a.x = logits;
+    a.tokens = tokens;
+    a.ldx = ldx;
+    a.experts = (int)experts;
+    a.topk = (int)topk;
+    a.sigmoid = (flags & TCM_ROUTE_SIGMOID) != 0;
+    a.norm = (flags & TCM_ROUTE_NORM) != 0;
+    a.bias = bias;
+    a.scale = scale;
+    a.ids = ids;
+    a.weights = weights;
+    char text[160];
+    snprintf(text, sizeof text, "kernel=route tokens=%lld experts=%lld topk=%lld dtype=%d%s%s%s", (long long)tokens,
+             (long long)experts, (long long)topk, t, a.sigmoid ? " sigmoid=1" : "", a.norm ? " norm=1" : "", bias ? " bias=1" : "");
+    set_last_plan(text);
+    return done(launch_route(t, a, stream));
+}
+
+int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t topk, const void* x, int64_t ldx,
+             const int* ids, const float* weights, const void* w1, const float* s1, const void* w2, const float* s2, void* out,
+             int64_t ldo, int dtype, void* stream) {
+    const int t = dtype & 0xff, flags = dtype & ~0xff;
+    const bool w8 = flags & TCM_W_E4M3;
+    if (t != F16 && t != BF16) return TCM_ERR_INVALID_VALUE;
+    // the output has x's type
+    if ((flags & ~TCM_W_E4M3) != (t == F16 ? TCM_C_F16 : TCM_C_BF16)) return TCM_ERR_INVALID_VALUE;
+    if (tokens < 0 || hidden < 0 || inter < 0 || experts < 0 || topk < 0) return TCM_ERR_INVALID_VALUE;
+    if (tokens >= kDim || hidden >= kDim || inter >= kDim || experts >= kDim || topk >= kDim) return TCM_ERR_INVALID_VALUE;
+    if (ldx < std::max<int64_t>(hidden, 1) || ldo < std::max<int64_t>(hidden, 1)) return TCM_ERR_INVALID_VALUE;
+    if (tokens == 0 || hidden == 0) {
+        set_last_plan("empty problem");
+        return TCM_OK;
+    }
+    const bool work = inter > 0 && experts > 0 && topk > 0;
+    if (!out || (work && (!x || !ids || !weights || !w1 || !w2 || (w8 && (!s1 || !s2))))) return TCM_ERR_INVALID_VALUE;
+    if (work && (!word_aligned(ids) || !word_aligned(weights) || (w8 && (!word_aligned(s1) || !word_aligned(s2)))))
+        return TCM_ERR_INVALID_VALUE;
+    const int64_t ws = w8 ? 1 : 2, pairs = span_of(tokens, topk, topk, 4);
+    const int64_t mat = span_of(hidden, inter, inter, 1), w2b = mat < 0 ? -1 : span_of(experts, mat, mat, ws);
+    const int64_t w1b = w2b < 0 || w2b > ((int64_t)1 << 60) ? -1 : 2 * w2b;
+    const int64_t xb = span_of(tokens, hidden, ldx, 2), ob = span_of(tokens, hidden, ldo, 2);
+    if (pairs < 0 || w1b < 0 || xb < 0 || ob < 0) return TCM_ERR_INVALID_VALUE;
+    const int64_t sbytes = w8 && work ? experts * scale_blocks(hidden) * scale_blocks(inter) * 4 : 0;
+    const Region o[1] = {{out, ob}};
+    const Region in[7] = {{x, work ? xb : 0}, {ids, pairs}, {weights, pairs}, {w1, w1b}, {w2, w2b}, {s1, 2 * sbytes}, {s2, sbytes}};
+    if (!disjoint(o, in)) return TCM_ERR_INVALID_VALUE;
+    MoeArgs a{};
+    a.ldx = ldx;
+    a.w1 = w1;
+    a.s1 = s1;
+    a.w2 = w2;
+    a.s2 = s2;
+    a.ldo = ldo;
+    a.hidden = (int)hidden;
+    a.inter = (int)inter;
+    a.experts = (int)experts;
+    a.topk = work ? (int)topk : 0;
+    char text[200];
+    // a launch counts its threads in 32 bits: tokens in chunks of 2^24 waves at most
+    const int64_t per_token = std::max<int64_t>(hidden, work ? topk * inter : 0);
+    const int64_t chunk = std::min<int64_t>(((int64_t)1 << 25) / per_token, tokens);
+    if (chunk == 0) return TCM_ERR_NOT_SUPPORTED;
+    snprintf(text, sizeof text, "kernel=moe_generic tokens=%lld hidden=%lld inter=%lld experts=%lld topk=%lld dtype=%d e4m3=%d",
+             (long long)tokens, (long long)hidden, (long long)inter, (long long)experts, (long long)topk, t, (int)w8);
+    set_last_plan(text);
+    for (int64_t t0 = 0; t0 < tokens; t0 += chunk) {
+        a.tokens = (int)std::min(chunk, tokens - t0);
+        a.x = (const char*)x + t0 * ldx * 2;
+        a.ids = ids + t0 * a.topk;
+        a.weights = weights + t0 * a.topk;
+        a.out = (char*)out + t0 * ldo * 2;
+        const int st = workspace_for(stream, std::max<int64_t>(moe_generic_workspace(a), 4), &a.ws);
+        if (st != TCM_OK) return st;
+        if (launch_moe_generic(t, w8, a, stream) != 0) return TCM_ERR_HIP;
+    }
+    return TCM_OK;
+}
+
+// nothing thrown on the host (memory, a lock) leaves a C entry
+template <class F>
+int guarded(F f) {
+    try {
+        return f();
+    } catch (const std::exception&) {
+        return TCM_ERR_ALLOC;
+    }
+}
+
+}  // namespace
+}  // namespace tcm
+
+using namespace tcm;
+
+extern "C" {
+
+int tcm_quantize_fp8(int64_t rows, int64_t cols, const void* X, int64_t ldx, int dtype, void* Q, int64_t ldq, float* S,
+                     int64_t lds, void* QT, int64_t ldqt, float* ST, int64_t ldst, void* stream) {
+    return guarded([&] { return quantize_impl(rows, cols, X, ldx, dtype, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream); });
+}
+
+int tcm_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa, const void* B,
+                 int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc, int dtype, const float* bias, int epilogue,
+                 void* stream) {
+    return guarded([&] { return gemm_fp8_impl(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, dtype, bias, epilogue, stream); });
+}
+
+int tcm_moe_route(int64_t tokens, int64_t experts, int64_t topk, const void* logits, int64_t ldx, int dtype, const float* bias,
+                  float scale, int32_t* ids, float* weights, void* stream) {
+    return guarded([&] { return route_impl(tokens, experts, topk, logits, ldx, dtype, bias, scale, ids, weights, stream); });
+}
+
+int tcm_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t topk, const void* X, int64_t ldx,
+            const int32_t* ids, const float* weights, const void* W1, const float* S1, const void* W2, const float* S2, void* out,
+            int64_t ldo, int dtype, void* stream) {
+    return guarded([&] {
+        return moe_impl(tokens, hidden, inter, experts, topk, X, ldx, ids, weights, W1, S1, W2, S2, out, ldo, dtype, stream);
+    });
+}
+
+}  // extern "C"

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/tcm.h"
+#include "lowp.h"
 #include "planner.h"
 #include "tcm_internal.h"
 
@@ -501,6 +502,20 @@ int check_problem(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int
 }
 
 }  // namespace
+
+int workspace_for(void* stream, int64_t bytes, void** out) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return TCM_ERR_HIP;
+    }
+    Workspace w;
+    const int st = get_workspace(dev, stream, bytes, 0, &w);
+    if (st == TCM_OK) *out = w.partial;
+    return st;
+}
+void set_last_plan(const char* text) { t_last_plan = text; }
+
 }  // namespace tcm
 
 using namespace tcm;
