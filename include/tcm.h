@@ -354,8 +354,14 @@ int tcm_quantize_fp8(int64_t rows, int64_t cols, const void* X, int64_t ldx, int
  *     C[m][n] = epi( [C_in[m][n] +] bias[n] +
  *                    sum_b sa[b][m] * sb[b, n] * sum_{k in block b} A[m][k] * B[n][k] ).
  *
- * A block's products are summed in binary32 on the matrix cores, multiplied
- * by its two scales and added to a binary32 accumulator.
+ * A block's products are summed on the matrix cores, multiplied by its two
+ * scales and added to a binary32 accumulator.  With C in f32 the block's sums
+ * are binary32 ones.  With C in 16 bits products of more than 64 rows may use
+ * the 8-bit matrix instructions, at twice the rate: these add eight products
+ * at a time after cutting each to 13 bits below the largest's leading one,
+ * and carry those sums in binary32.  That is off by 2^-16 of the sum of the
+ * products' magnitudes at most on ordinary data (2^-10 in the worst case),
+ * where C's own rounding is off by 2^-8 (bf16) or 2^-11 (f16) of a value.
  *
  *   M, N, K      sizes, 0 <= size < 2^31; empty and K == 0 as tcm_gemm.
  *   A, lda       M x K, k contiguous, lda >= K; e4m3 or, with TCM_A_E5M2, e5m2.
@@ -493,6 +499,12 @@ const char* tcm_status_string(int status);
  *                  of 64 rows, at most 1024 each (4x4x4 kernel), of 128
  *                  rows (16x16x32 row-major kernel) or of 256 rows
  *                  (column-major B) (1..4096).
+ *   "fp8_config"   tcm_gemm_fp8's kernel: -1 = planner decides, 0 .. 3 = the
+ *                  256x256, 256x128, 128x128 or 64x128 tile (f32 C: not the
+ *                  first), 4 = the any-alignment kernel; a kernel that cannot
+ *                  serve the call is ignored.
+ *   "fp8_split"    0 = planner decides, else the k ranges each of its tiles
+ *                  is cut into (1..64, at most one a 128-wide block).
  * Unknown keys or out-of-range values: TCM_ERR_INVALID_VALUE.
  * tcm_get_option returns the value, or -2 for an unknown key.
  */

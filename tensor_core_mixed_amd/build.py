@@ -24,7 +24,11 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 # Per-source flags.  The GEMV kernels take their matrix-core accumulators in
 # the architectural registers: with the accumulation registers the compiler
 # copied the 64-row kernel's 128 accumulators out and back every step.
-EXTRA_FLAGS = {"gemv_kernel.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# The 8-bit tiles scale their matrix-core results on the vector ALU, which
+# reads architectural registers only.
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA_FLAGS = {f: _VGPR_FORM for f in ("gemv_kernel.hip", "fp8_tile_e4m3_e4m3.hip", "fp8_tile_e4m3_e5m2.hip",
+                                       "fp8_tile_e5m2_e4m3.hip", "fp8_tile_e5m2_e5m2.hip")}
 
 
 def sources():

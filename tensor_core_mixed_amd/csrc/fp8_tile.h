@@ -1,0 +1,520 @@
+// Tiled kernel of the block-scaled 8-bit product,
+//
+//     C[m][n] = epi(init + sum over blocks b of 128 k of
+//                          (sa[b][m] * sb[b, n]) * P_b[m][n]),
+//     P_b[m][n] = sum over the block's k of A[m][k] * B[n][k].
+//
+// One scale block is one K-step and one matrix instruction deep: a
+// 16x16x128 8-bit MFMA with a zero accumulator gives P_b of a 16 x 16 tile
+// whole, and four multiply-adds a lane add it, scaled, to the binary32
+// accumulator while the next MFMA runs (the MFMA holds the matrix core for 32
+// cycles, the multiply-adds the vector ALU for 16; with a scale of its own for
+// every row of B the factor is one more multiplication each, 32).  The MFMA's
+// own block exponents are not used: the scales are arbitrary binary32 values.
+//
+// The MFMA takes its A operand from B's rows and its B operand from A's, so a
+// lane's accumulators run along n at one m: sa is one value a lane and tile,
+// and stores are contiguous.  B's rows are dealt to the 16-row tiles of a
+// wave's 64 columns as n = 16 * (i / 4) + 4 * tile + i % 4: a lane then holds
+// 16 consecutive columns of a row.  (Which k an operand register holds plays
+// no part as long as both operands agree.)
+//
+// Copies, LDS layout and pipeline are the dense kernels': 128-byte rows of
+// each operand go to LDS by 16-byte direct loads, the chunk index XOR-ed with
+// a function of the row so that the reads of a fragment fall on distinct
+// banks; STAGES stages, copies STAGES - 1 steps ahead.  The scales of a step
+// travel with it (4-byte direct loads).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "fp8_util.h"
+#include "lowp.h"
+
+namespace tcm {
+namespace fp8t {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef int i8v __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr unsigned kOOB = 0x40000000u;  // past every descriptor's range: such loads give zeros
+constexpr int kRsrcWord3 = 0x00020000;  // raw dword access
+
+// bytes [0, n) of a chunk, the others zero
+__device__ __forceinline__ i4 keep_bytes(i4 v, int n) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int k = n - 4 * d;
+        v[d] = k >= 4 ? v[d] : (k <= 0 ? 0 : (int)((unsigned)v[d] & (0xffffffffu >> (32 - 8 * k))));
+    }
+    return v;
+}
+
+// One lane's 32 bytes of an operand as the matrix instruction takes them: the
+// bytes themselves, or (WIDE) 16-bit floats, which hold both formats exactly.
+template <bool WIDE>
+struct Operand {
+    i8v v;
+};
+template <>
+struct Operand<true> {
+    h8 v[4];
+};
+template <bool E5, bool WIDE>
+__device__ __forceinline__ Operand<WIDE> operand(i8v x) {
+    Operand<WIDE> o;
+    if constexpr (!WIDE) {
+        o.v = x;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o.v[q] = fp8_to_f16x8<E5>(x[2 * q], x[2 * q + 1]);
+    }
+    return o;
+}
+template <bool A5, bool B5, bool WIDE>
+__device__ __forceinline__ f4 mma(const Operand<WIDE>& b, const Operand<WIDE>& a) {
+    f4 p = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (!WIDE) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, p, B5 ? 1 : 0, A5 ? 1 : 0, 0, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[q], a.v[q], p, 0, 0, 0);
+        return p;
+    }
+}
+
+// 16 consecutive columns n .. n+15 of row m: accumulators to C
+struct Epilogue {
+    // v[16] += bias and C's contents, ReLU, store; full: all 16 columns exist
+    __device__ __forceinline__ static void row16(const Fp8Args& a, float (&v)[16], int64_t m, int64_t n) {
+        const bool full = n + 16 <= a.N;
+        if (a.has_bias) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (full || n + j < a.N) v[j] += load_float<F32>((const char*)a.bias, n + j);
+        }
+        char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
+        const int cs = c_elem_bytes(a.c_type);
+        if (a.accum) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (full || n + j < a.N) v[j] += load_c_any(c + j * cs, a.c_type);
+        }
+        if (a.relu) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = v[j] > 0.f ? v[j] : 0.f;
+        }
+        if (full && a.c_vec) {
+            if (a.c_type == C_ACC) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) *(f4*)(c + 16 * q) = f4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            } else {
+                i4 w[2];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    unsigned lo, hi;
+                    if (a.c_type == C_F16) {
+                        lo = __builtin_bit_cast(unsigned short, (_Float16)v[2 * q]);
+                        hi = __builtin_bit_cast(unsigned short, (_Float16)v[2 * q + 1]);
+                    } else {
+                        lo = __builtin_bit_cast(unsigned short, (__bf16)v[2 * q]);
+                        hi = __builtin_bit_cast(unsigned short, (__bf16)v[2 * q + 1]);
+                    }
+                    w[q >> 2][q & 3] = (int)(lo | hi << 16);
+                }
+                *(i4*)c = w[0];
+                *(i4*)(c + 16) = w[1];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n + j < a.N) store_c_any(c + j * cs, a.c_type, v[j]);
+        }
+    }
+};
+
+template <int CFG, bool A5, bool B5, bool BROW, bool WIDE>
+struct Tile {
+    static constexpr Fp8Tile cfg = kFp8Tiles[CFG];
+    static constexpr int BM = cfg.bm, BN = cfg.bn, WM = cfg.wm, WN = cfg.wn, NST = cfg.stages;
+    static constexpr int NW = WM * WN, NT = NW * 64;
+    static constexpr int TM = BM / WM, FM = TM / 16;  // 16-row tiles of A a wave
+    static_assert(BN / WN == 64, "a wave covers 64 columns");
+    static constexpr int GM = FM >= 4 ? 2 : 1, NG = FM / GM;        // row tiles taken together, groups a K-step
+    static_assert(FM % (2 * GM) == 0, "a step starts with the first of the two fragment buffers");
+    // waves 0-3 of eight copy the operands and waves 4-7 the scales; of four every wave copies its share of both
+    static constexpr int NWC = 4;
+    static_assert(NW == 8 || NW == 4, "");
+    static constexpr int IA = BM / (8 * NWC), IB = BN / (8 * NWC);
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + 1024;
+    static constexpr int STAGE = SB_OFF + 1024;
+    static constexpr int LDS = NST * STAGE;
+    static_assert(LDS <= 160 * 1024 && BM <= 256 && BN <= 256, "");
+
+    // rows of A are read 16 at a time at one chunk, rows of B four by four at a distance of 16
+    __device__ __forceinline__ static int swz_a(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+    __device__ __forceinline__ static int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 4) & 3) << 1; }
+
+    // this lane's offsets in the copies of a step, and where the next step to copy begins
+    struct Dma {
+        unsigned a_off, b_off[2], sa_off, sb_off;
+        int a_k, b_k[2];
+        const unsigned char *pa, *pb;
+        const float *psa, *psb;
+        int64_t sa_step, sb_step;  // floats
+        unsigned a_hop, b_hop;
+        int a_range, b_range, k_left;
+    };
+    __device__ __forceinline__ static void dma_setup(Dma& d, const Fp8Args& a, int64_t m0, int64_t n0, int k_lo, int wave, int lane) {
+        const int w = wave & 3;
+        {
+            const int r = 8 * w + (lane >> 3), c = (lane & 7) ^ swz_a(r);
+            d.a_off = (unsigned)(r * (int)a.lda + 16 * c);
+            d.a_k = 16 * c;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {  // (the swizzle of rows 32 apart differs: two offsets)
+            const int r = 8 * (4 * q + w) + (lane >> 3), c = (lane & 7) ^ swz_b(r);
+            d.b_off[q] = (unsigned)(r * (int)a.ldb + 16 * c);
+            d.b_k[q] = 16 * c;
+        }
+        const int i = 64 * w + lane;
+        d.sa_off = i < BM && m0 + i < a.M ? (unsigned)(4 * i) : kOOB;
+        d.sb_off = i >= BN || n0 + i >= a.N ? kOOB : (BROW ? (unsigned)(4 * i) : (unsigned)(((i + (int)(n0 & 127)) >> 7) * (int)a.ldsb * 4));
+        const int64_t k0 = (int64_t)k_lo * 128;
+        d.pa = a.A + m0 * a.lda + k0;
+        d.pb = a.B + n0 * a.ldb + k0;
+        d.psa = a.sa + k_lo * a.ldsa + m0;
+        d.psb = BROW ? a.sb + k_lo * a.ldsb + n0 : a.sb + n0 / 128 * a.ldsb + k_lo;
+        d.sa_step = a.ldsa;
+        d.sb_step = BROW ? a.ldsb : 1;
+        d.a_hop = (unsigned)(32 * (int)a.lda);
+        d.b_hop = (unsigned)(64 * (int)a.ldb);
+        // the ranges end with the last row's last 16-byte chunk (which may hold bytes past K)
+        const int left = (int)(a.K - k0);
+        const int rows_a = min((int)a.M - (int)m0, BM), rows_b = min((int)a.N - (int)n0, BN);
+        d.a_range = (rows_a - 1) * (int)a.lda + ((left + 15) & ~15);
+        d.b_range = (rows_b - 1) * (int)a.ldb + ((left + 15) & ~15);
+        d.k_left = left;
+    }
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc(const void* p, int n) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, n, kRsrcWord3);
+    }
+    // the copies of the next K-step into stage st
+    __device__ __forceinline__ static void dma_issue(Dma& d, lds_char* smem, int st, int wave) {
+        const int w = wave & 3;
+        lds_char* s = smem + st * STAGE;
+        if (NW == 4 || wave < 4) {
+            const __amdgpu_buffer_rsrc_t ra = rsrc(d.pa, d.a_range), rb = rsrc(d.pb, d.b_range);
+            const unsigned oa = d.a_k < d.k_left ? d.a_off : kOOB;
+            const unsigned ob[2] = {d.b_k[0] < d.k_left ? d.b_off[0] : kOOB, d.b_k[1] < d.k_left ? d.b_off[1] : kOOB};
+#pragma unroll
+            for (int j = 0; j < IA; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(s + (4 * j + w) * 1024), 16, oa, j * d.a_hop, 0, 0);
+#pragma unroll
+            for (int j = 0; j < IB; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(s + A_BYTES + (4 * j + w) * 1024), 16, ob[j & 1],
+                                                         (j >> 1) * d.b_hop, 0, 0);
+        }
+        if (NW == 4 || wave >= 4) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.psa, BM * 4), (lds_void*)(s + SA_OFF + w * 256), 4, d.sa_off, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.psb, (int)kOOB), (lds_void*)(s + SB_OFF + w * 256), 4, d.sb_off, 0, 0, 0);
+        }
+        d.pa += 128;
+        d.pb += 128;
+        d.psa += d.sa_step;
+        d.psb += d.sb_step;
+        d.a_range -= 128;
+        d.b_range -= 128;
+        d.k_left -= 128;
+    }
+    // until at most `steps` K-steps of this wave's copies are in flight, and every LDS read has returned
+    __device__ __forceinline__ static void wait_copies(int steps, int wave) {
+        constexpr int OP = IA + IB;
+        if constexpr (NST > 2) {
+            if (steps >= 1) {
+                if (NW == 4) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(OP + 2) : "memory");
+                else if (wave < 4) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(OP) : "memory");
+                else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)" ::: "memory");
+                return;
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    }
+    static_assert(NST <= 3, "wait_copies");
+
+    // The last step of a K that is no multiple of 16: zeros for the bytes past K of the chunk that K ends in.
+    __device__ __forceinline__ static void mask_tail(lds_char* smem, int st, int krem, int tid) {
+        const int c = krem >> 4;
+        for (int r = tid; r < BM + BN; r += NT) {
+            const int x = r < BM ? swz_a(r) : swz_b(r - BM);
+            __attribute__((address_space(3))) i4* p =
+                (__attribute__((address_space(3))) i4*)(smem + st * STAGE + r * 128 + ((c ^ x) << 4));
+            *p = keep_bytes(*p, krem & 15);
+        }
+        __syncthreads();
+    }
+
+    struct Lane {
+        int a[2], b[2];   // byte offsets within a stage of this lane's two chunks of row tile 0
+        int sa, sb;
+    };
+    __device__ __forceinline__ static i8v read_pair(const lds_char* s, int o0, int o1) {
+        const i4 x = *(const __attribute__((address_space(3))) i4*)(s + o0);
+        const i4 y = *(const __attribute__((address_space(3))) i4*)(s + o1);
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ __forceinline__ static float lds_f(const lds_char* s, int o) {
+        return *(const __attribute__((address_space(3))) float*)(s + o);
+    }
+
+    struct Rows {  // a group of row tiles
+        i8v a[GM];
+        float s[GM];
+    };
+    struct Cols {
+        i8v b[4];
+        f4 s[BROW ? 4 : 1];
+    };
+    __device__ __forceinline__ static void read_rows(Rows& f, const lds_char* s, const Lane& l, int g) {
+#pragma unroll
+        for (int i = 0; i < GM; ++i) {
+            f.a[i] = read_pair(s, l.a[0] + (g * GM + i) * 2048, l.a[1] + (g * GM + i) * 2048);
+            f.s[i] = lds_f(s, l.sa + (g * GM + i) * 64);
+        }
+    }
+    __device__ __forceinline__ static void read_col(Cols& f, const lds_char* s, const Lane& l, int j) {
+        f.b[j] = read_pair(s, l.b[0] + j * 512, l.b[1] + j * 512);
+    }
+    __device__ __forceinline__ static void read_scales(Cols& f, const lds_char* s, const Lane& l) {
+        if constexpr (BROW) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.s[j] = *(const __attribute__((address_space(3))) f4*)(s + l.sb + 16 * j);
+        } else {
+            f.s[0][0] = lds_f(s, l.sb);
+        }
+    }
+    __device__ __forceinline__ static void scale_add(f4& acc, f4 p, float sa, const Cols& f, int j) {
+        if constexpr (BROW) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(p[r], sa * f.s[j][r], acc[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(p[r], sa, acc[r]);  // (sa times the tile's scale)
+        }
+    }
+
+    // (keeps the compiler from sinking multiply-adds past the branches of the pipeline)
+    __device__ __forceinline__ static void pin(f4& v) { asm volatile("" : "+v"(v)); }
+
+    // K-steps [k_lo, k_hi) of tile (m0, n0)
+    __device__ __forceinline__ static void mainloop(f4 (&acc)[FM][4], const Fp8Args& a, lds_char* smem, int64_t m0, int64_t n0,
+                                                    int k_lo, int k_hi, int wave, int lane) {
+        const int wm = wave / WN, wn = wave % WN;
+        Dma d;
+        dma_setup(d, a, m0, n0, k_lo, wave, lane);
+        Lane l;
+        {
+            const int i = lane & 15, g = lane >> 4;
+            const int ra = wm * TM + i, rb = wn * 64 + 16 * (i >> 2) + (i & 3);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                l.a[q] = ra * 128 + (((g + 4 * q) ^ swz_a(ra)) << 4);
+                l.b[q] = A_BYTES + rb * 128 + (((g + 4 * q) ^ swz_b(rb)) << 4);
+            }
+            l.sa = SA_OFF + ra * 4;
+            l.sb = SB_OFF + (wn * 64 + (BROW ? 16 * g : 0)) * 4;
+        }
+        const int k_tail = (a.K & 15) ? (int)(a.K & 127) : 0;  // the step that needs mask_tail is the matrix's last
+        const int last = (int)((a.K + 127) / 128) - 1;
+        const int first = min(NST, k_hi - k_lo);
+#pragma unroll
+        for (int i = 0; i < NST; ++i)
+            if (i < first) dma_issue(d, smem, i, wave);
+        wait_copies(0, wave);
+        __syncthreads();
+        if (k_tail && k_lo == last) mask_tail(smem, 0, k_tail, threadIdx.x);
+        Rows fr[2];
+        Cols fc;
+        Operand<WIDE> ob[4];
+        read_rows(fr[0], smem, l, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) read_col(fc, smem, l, j);
+        read_scales(fc, smem, l);
+        int st = 0;
+        for (int kt = k_lo; kt < k_hi; ++kt) {
+            const lds_char* s = smem + st * STAGE;
+            const int sn = st + 1 == NST ? 0 : st + 1;
+            const lds_char* nx = smem + sn * STAGE;
+            f4 p[2][GM];
+            float t[2][GM];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                Rows& cur = fr[g & 1];
+                Rows& nxt = fr[(g + 1) & 1];
+                const bool end = g == NG - 1;
+#pragma unroll
+                for (int i = 0; i < GM; ++i) t[g & 1][i] = BROW ? cur.s[i] : cur.s[i] * fc.s[0][0];
+                Operand<WIDE> oa[GM];
+#pragma unroll
+                for (int i = 0; i < GM; ++i) oa[i] = operand<A5, WIDE>(cur.a[i]);
+                if (!end) {
+                    read_rows(nxt, s, l, g + 1);
+                } else {
+                    // every fragment of this step is in registers: the next step's copies must have landed, and those
+                    // of step kt + NST may overwrite this stage
+#pragma unroll
+                    for (int i = 0; i < FM - GM; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) pin(acc[i][j]);
+                    wait_copies(kt + NST <= k_hi ? NST - 2 : 0, wave);
+                    __syncthreads();
+                    if (kt + NST < k_hi) dma_issue(d, smem, st, wave);
+                    if (k_tail && kt + 1 == last && kt + 1 < k_hi) mask_tail(smem, sn, k_tail, threadIdx.x);
+                    read_rows(nxt, nx, l, 0);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int q = g * 4 + j;
+                    if (g == 0) ob[j] = operand<B5, WIDE>(fc.b[j]);
+#pragma unroll
+                    for (int i = 0; i < GM; ++i) p[q & 1][i] = mma<A5, B5, WIDE>(ob[j], oa[i]);
+                    if (end) read_col(fc, nx, l, j);
+                    if (q > 0) {  // the products before these
+                        const int g1 = (q - 1) >> 2, j1 = (q - 1) & 3;
+#pragma unroll
+                        for (int i = 0; i < GM; ++i) scale_add(acc[g1 * GM + i][j1], p[(q - 1) & 1][i], t[g1 & 1][i], fc, j1);
+                    }
+                    // in turn one product and the multiply-adds of the one GM before it
+#pragma unroll
+                    for (int i = 0; i < GM; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
+                        if (end) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        else if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < GM; ++i) scale_add(acc[FM - GM + i][3], p[1][i], t[(NG - 1) & 1][i], fc, 3);
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pin(acc[i][j]);
+            read_scales(fc, nx, l);
+            st = sn;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+
+    __device__ __forceinline__ static void run(const Fp8Args& a) {
+        __shared__ __attribute__((aligned(1024))) char smem_raw[LDS];
+        lds_char* smem = (lds_char*)smem_raw;
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave / WN, wn = wave % WN;
+        const int T = a.tiles_m * a.tiles_n;
+        const int nidx = xcd_order(blockIdx.x, T * a.split);
+        const int share = nidx / T, t = nidx - share * T;
+        int tm, tn;
+        super_order(t, a.tiles_m, a.tiles_n, a.group_m, a.super_m, a.super_n, &tm, &tn);
+        const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+        const int64_t steps = (a.K + 127) / 128;
+        const int k_lo = (int)(share * steps / a.split), k_hi = (int)((share + 1) * steps / a.split);
+        f4 acc[FM][4];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+        if (k_lo < k_hi) mainloop(acc, a, smem, m0, n0, k_lo, k_hi, wave, lane);
+        if (a.split > 1) {
+            f4* o = (f4*)a.ws + ((int64_t)nidx * NW + wave) * FM * 4 * 64 + lane;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[(i * 4 + j) * 64] = acc[i][j];
+            return;
+        }
+        const int64_t n = n0 + wn * 64 + 16 * (lane >> 4);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int64_t m = m0 + wm * TM + 16 * i + (lane & 15);
+            if (m >= a.M || n >= a.N) continue;
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = acc[i][e >> 2][e & 3];
+            Epilogue::row16(a, v, m, n);
+        }
+    }
+
+    // Sum of a split launch: one wave takes the 16 rows x 64 columns of one (tile, wave, row tile), adds the shares'
+    // partials in order and stores them.
+    __device__ __forceinline__ static void run_sum(const Fp8Args& a) {
+        const int lane = threadIdx.x & 63;
+        const int64_t T = (int64_t)a.tiles_m * a.tiles_n;
+        int64_t b = blockIdx.x;
+        const int i = (int)(b % FM);
+        b /= FM;
+        const int wave = (int)(b % NW);
+        const int t = (int)(b / NW);
+        int tm, tn;
+        super_order(t, a.tiles_m, a.tiles_n, a.group_m, a.super_m, a.super_n, &tm, &tn);
+        const int wm = wave / WN, wn = wave % WN;
+        const int64_t m = (int64_t)tm * BM + wm * TM + 16 * i + (lane & 15), n = (int64_t)tn * BN + wn * 64 + 16 * (lane >> 4);
+        if (m >= a.M || n >= a.N) return;
+        const f4* p = (const f4*)a.ws + (((int64_t)t * NW + wave) * FM + i) * 4 * 64 + lane;
+        const int64_t step = T * NW * FM * 4 * 64;
+        f4 s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = p[j * 64];
+        for (int k = 1; k < a.split; ++k) {
+            p += step;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += p[j * 64];
+        }
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = s[e >> 2][e & 3];
+        Epilogue::row16(a, v, m, n);
+    }
+};
+
+template <int CFG, bool A5, bool B5, bool BROW, bool WIDE>
+__global__ __launch_bounds__((Tile<CFG, A5, B5, BROW, WIDE>::NT)) __attribute__((amdgpu_waves_per_eu(2)))
+void fp8_tile_kernel(Fp8Args a) {
+    Tile<CFG, A5, B5, BROW, WIDE>::run(a);
+}
+
+template <int CFG, bool A5, bool B5, bool WIDE>
+void launch_width(const Fp8Args& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n * a.split)), block(Tile<CFG, A5, B5, false, WIDE>::NT);
+    if (a.b_row) hipLaunchKernelGGL((fp8_tile_kernel<CFG, A5, B5, true, WIDE>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((fp8_tile_kernel<CFG, A5, B5, false, WIDE>), grid, block, 0, s, a);
+}
+template <int CFG, bool A5, bool B5>
+int launch_cfg(const Fp8Args& a, hipStream_t s) {
+    if constexpr (kFp8Tiles[CFG].wide) {
+        if (a.c_type == C_ACC) launch_width<CFG, A5, B5, true>(a, s);
+        else launch_width<CFG, A5, B5, false>(a, s);
+    } else {
+        if (a.c_type == C_ACC) return -1;
+        launch_width<CFG, A5, B5, false>(a, s);
+    }
+    return (int)hipGetLastError();
+}
+template <bool A5, bool B5>
+int launch_types(int cfg, const Fp8Args& a, hipStream_t s) {
+    static_assert(kNumFp8Tiles == 4, "one case a config");
+    switch (cfg) {
+    case 0: return launch_cfg<0, A5, B5>(a, s);
+    case 1: return launch_cfg<1, A5, B5>(a, s);
+    case 2: return launch_cfg<2, A5, B5>(a, s);
+    default: return launch_cfg<3, A5, B5>(a, s);
+    }
+}
+
+}  // namespace fp8t
+}  // namespace tcm

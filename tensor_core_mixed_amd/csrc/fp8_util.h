@@ -31,6 +31,28 @@ __device__ __forceinline__ unsigned fp8_encode4(float a, float b, float c, float
     return (unsigned)w;
 }
 
+// eight bytes to eight binary16 values: exact, NaN and infinity kept (an e5m2
+// byte is the upper half of the binary16 value)
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+template <bool E5M2>
+__device__ __forceinline__ f16x8_t fp8_to_f16x8(int w0, int w1) {
+    f16x2_t h[4];
+    if constexpr (E5M2) {
+        h[0] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm((unsigned)w0, (unsigned)w0, 0x010c000cu));
+        h[1] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm((unsigned)w0, (unsigned)w0, 0x030c020cu));
+        h[2] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm((unsigned)w1, (unsigned)w1, 0x010c000cu));
+        h[3] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm((unsigned)w1, (unsigned)w1, 0x030c020cu));
+    } else {
+        h[0] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false));
+        h[1] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true));
+        h[2] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false));
+        h[3] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true));
+    }
+    return __builtin_shufflevector(__builtin_shufflevector(h[0], h[1], 0, 1, 2, 3), __builtin_shufflevector(h[2], h[3], 0, 1, 2, 3), 0, 1, 2,
+                                   3, 4, 5, 6, 7);
+}
+
 // element i of a 16- or 32-bit float array at any address
 template <int XT>
 __device__ __forceinline__ float load_float(const char* base, int64_t i) {

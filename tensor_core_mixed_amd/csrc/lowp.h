@@ -40,9 +40,33 @@ struct Fp8Args {
     int64_t M, N, K, lda, ldb, ldc, ldsa, ldsb;
     int a_e5m2, b_e5m2, b_row;
     int has_bias, relu, accum, c_type;
+    // the tiled kernels
+    int c_vec;                       // C's rows at multiples of 16 bytes
+    int tiles_m, tiles_n;
+    int group_m, super_m, super_n;   // tile order (tile_coords)
+    int split;                       // k ranges of a tile, summed by a second launch
+    float* ws;                       // their partial tiles
 };
 // any alignment, leading dimension and size
 int launch_fp8_generic(const Fp8Args& a, void* stream);
+// Macro tiles of the tiled kernel: waves WM x WN of (BM/WM) x 64 outputs, LDS stages of 128 k.
+struct Fp8Tile {
+    int bm, bn, wm, wn, stages;
+    bool wide;  // serves binary32 C (products on 16-bit operands, which take more registers)
+};
+constexpr int kNumFp8Tiles = 4;
+constexpr Fp8Tile kFp8Tiles[kNumFp8Tiles] = {
+    {256, 256, 2, 4, 2, false},  // large products: 128 x 64 a wave, two waves a SIMD
+    {256, 128, 4, 2, 3, true},  // half as many columns, three stages
+    {128, 128, 2, 2, 2, true},  // two workgroups a CU
+    {64, 128, 2, 2, 2, true},   // few rows
+};
+// A, B and sizes as fp8_tiles_fit accepts; the operand types pick the instance
+int launch_fp8_tile_e4m3_e4m3(int cfg, const Fp8Args& a, void* stream);
+int launch_fp8_tile_e5m2_e4m3(int cfg, const Fp8Args& a, void* stream);
+int launch_fp8_tile_e4m3_e5m2(int cfg, const Fp8Args& a, void* stream);
+int launch_fp8_tile_e5m2_e5m2(int cfg, const Fp8Args& a, void* stream);
+int launch_fp8_tile_sum(int cfg, const Fp8Args& a, void* stream);
 
 struct RouteArgs {
     const void* x;         // [tokens][experts]
@@ -74,6 +98,14 @@ struct MoeArgs {
 int64_t moe_generic_workspace(const MoeArgs& a);
 int launch_moe_generic(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
 
+// Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the
+// planner's choice, else a row of kFp8Tiles or kFp8Generic; and the k ranges
+// of a tile, 0 the planner's choice.
+constexpr int kFp8Generic = kNumFp8Tiles, kFp8MaxSplit = 64;
+struct LowpOpts {
+    int fp8_config = -1, fp8_split = 0;
+};
+LowpOpts lowp_opts();
 // Shared with the C ABI's other entry points (tcm_api.cpp): the stream's
 // workspace, grown to `bytes` (a tcm_status), and the text of tcm_last_plan.
 int workspace_for(void* stream, int64_t bytes, void** out);

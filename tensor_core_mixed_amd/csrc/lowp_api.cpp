@@ -91,6 +91,51 @@ int quantize_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dt
     return done(launch_quantize(t, flags & TCM_Q_E5M2, tile, a, stream));
 }
 
+// Sizes, strides and alignment that the tiled kernels take: 16-byte rows of A
+// and B, and a macro tile's rows within a buffer descriptor's range (2^30).
+bool fp8_tiles_fit(const Fp8Args& a) {
+    const int64_t lim = ((int64_t)1 << 30) / 256;
+    return a.K > 0 && a.K <= ((int64_t)1 << 30) && !((uintptr_t)a.A & 15) && !((uintptr_t)a.B & 15) && !(a.lda & 15) &&
+           !(a.ldb & 15) && a.lda < lim && a.ldb < lim && a.ldsb < ((int64_t)1 << 26);
+}
+// The macro tile and the k ranges of a product by a model of its time, in
+// microseconds: a workgroup's K-steps, one at a time on a CU or `per_cu` of
+// them sharing it, and for a split the sum's launch and the partial tiles'
+// way through the caches.  Step times fitted to products of 64 to 8192 rows,
+// 8-bit and (binary32 C) 16-bit operands.
+struct Fp8Plan {
+    int config, split;
+};
+Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
+    static constexpr struct {
+        int per_cu;
+        double lone, shared, lone_wide, shared_wide;
+    } kStep[kNumFp8Tiles] = {{1, 2.0, 2.0, 0, 0}, {1, 1.1, 1.25, 2.3, 2.7}, {2, 0.75, 1.15, 1.3, 2.3}, {2, 0.6, 0.78, 0.8, 1.35}};
+    constexpr double kFixed = 3.0, kSum = 4.0, kBytesPerUs = 5e6;
+    Fp8Plan best{kFp8Generic, 1};
+    if (!fp8_tiles_fit(a) || o.fp8_config == kFp8Generic) return best;
+    const bool wide = a.c_type == C_ACC;
+    const int64_t steps = scale_blocks(a.K);
+    double best_t = 1e30;
+    for (int c = 0; c < kNumFp8Tiles; ++c) {
+        const Fp8Tile& t = kFp8Tiles[c];
+        if (wide && !t.wide) continue;
+        if (o.fp8_config >= 0 && c != o.fp8_config && (!wide || kFp8Tiles[o.fp8_config].wide)) continue;
+        const int64_t tiles = ((a.M + t.bm - 1) / t.bm) * ((a.N + t.bn - 1) / t.bn);
+        const double lone = wide ? kStep[c].lone_wide : kStep[c].lone, shared = wide ? kStep[c].shared_wide : kStep[c].shared;
+        const int64_t slots = 256 * kStep[c].per_cu;
+        for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
+            if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
+            const int64_t wgs = tiles * s, rest = wgs % slots;
+            const double step = (double)(wgs / slots) * shared + (rest == 0 ? 0 : (rest <= 256 ? lone : shared));
+            const double time = kFixed + (double)((steps + s - 1) / s) * step +
+                                (s > 1 ? kSum + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            if (time < best_t) best_t = time, best = {c, s};
+        }
+    }
+    return best;
+}
+
 int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* sa, int64_t ldsa, const void* B,
                   int64_t ldb, const float* sb, int64_t ldsb, void* C, int64_t ldc, int dtype, const float* bias, int epilogue,
                   void* stream) {
@@ -140,12 +185,37 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
     a.relu = (epilogue & TCM_EPI_RELU) != 0;
     a.accum = (epilogue & TCM_EPI_ACCUM) != 0;
     a.c_type = c_type;
+    a.c_vec = ((uintptr_t)C & 15) == 0 && ((ldc * c_elem_bytes(c_type)) & 15) == 0;
     char text[160];
-    // (a launch counts its threads in 32 bits)
-    if (((M + 63) / 64) * ((N + 63) / 64) >= ((int64_t)1 << 24)) return TCM_ERR_NOT_SUPPORTED;
-    snprintf(text, sizeof text, "kernel=fp8_generic M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+    const Fp8Plan pl = plan_fp8(a, lowp_opts());
+    if (pl.config == kFp8Generic) {
+        // (a launch counts its threads in 32 bits)
+        if (((M + 63) / 64) * ((N + 63) / 64) >= ((int64_t)1 << 24)) return TCM_ERR_NOT_SUPPORTED;
+        snprintf(text, sizeof text, "kernel=fp8_generic M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+        set_last_plan(text);
+        return done(launch_fp8_generic(a, stream));
+    }
+    const Fp8Tile& t = kFp8Tiles[pl.config];
+    const int64_t tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
+    if (tm * tn * pl.split >= ((int64_t)1 << 22)) return TCM_ERR_NOT_SUPPORTED;
+    a.tiles_m = (int)tm;
+    a.tiles_n = (int)tn;
+    a.group_m = 4;
+    tile_order_shape(a.tiles_m, a.tiles_n, a.group_m, &a.super_m, &a.super_n);
+    a.split = pl.split;
+    if (a.split > 1) {
+        void* ws = nullptr;
+        const int st = workspace_for(stream, tm * tn * a.split * t.bm * t.bn * 4, &ws);
+        if (st != TCM_OK) return st;
+        a.ws = (float*)ws;
+    }
+    snprintf(text, sizeof text, "kernel=fp8_tile tile=%dx%d tiles=%lld split=%d M=%lld N=%lld K=%lld", t.bm, t.bn,
+             (long long)(tm * tn), a.split, (long long)M, (long long)N, (long long)K);
     set_last_plan(text);
-    return done(launch_fp8_generic(a, stream));
+    const auto launch = a.a_e5m2 ? (a.b_e5m2 ? launch_fp8_tile_e5m2_e5m2 : launch_fp8_tile_e5m2_e4m3)
+                                 : (a.b_e5m2 ? launch_fp8_tile_e4m3_e5m2 : launch_fp8_tile_e4m3_e4m3);
+    if (launch(pl.config, a, stream) != 0) return TCM_ERR_HIP;
+    return done(a.split > 1 ? launch_fp8_tile_sum(pl.config, a, stream) : 0);
 }
 
 int route_impl(int64_t tokens, int64_t experts, int64_t topk, const void* logits, int64_t ldx, int dtype, const float* bias,

@@ -503,6 +503,13 @@ int check_problem(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int
 
 }  // namespace
 
+namespace {
+LowpOpts g_lowp;  // (guarded by g_mu)
+}
+LowpOpts lowp_opts() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    return g_lowp;
+}
 int workspace_for(void* stream, int64_t bytes, void** out) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) {
@@ -574,6 +581,12 @@ int tcm_set_option(const char* key, int64_t value) {
     } else if (!strcmp(key, "gemv_wide")) {
         if (value < 0 || value > 2) return TCM_ERR_INVALID_VALUE;
         g_opts.gemv_wide = (int)value;
+    } else if (!strcmp(key, "fp8_config")) {
+        if (value < -1 || value > kFp8Generic) return TCM_ERR_INVALID_VALUE;
+        g_lowp.fp8_config = (int)value;
+    } else if (!strcmp(key, "fp8_split")) {
+        if (value < 0 || value > kFp8MaxSplit) return TCM_ERR_INVALID_VALUE;
+        g_lowp.fp8_split = (int)value;
     } else {
         return TCM_ERR_INVALID_VALUE;
     }
@@ -595,6 +608,8 @@ int64_t tcm_get_option(const char* key) {
     if (!strcmp(key, "gemv")) return g_opts.gemv;
     if (!strcmp(key, "gemv_splits")) return g_opts.gemv_splits;
     if (!strcmp(key, "gemv_wide")) return g_opts.gemv_wide;
+    if (!strcmp(key, "fp8_config")) return g_lowp.fp8_config;
+    if (!strcmp(key, "fp8_split")) return g_lowp.fp8_split;
     return -2;
 }
 

@@ -156,6 +156,15 @@ def run_gemm(M, N, K, ta=E4M3, tb=E4M3, c=torch.float32, b_row=False, bias=False
     return got[:, :N], ref, bound + half_step(ref, c) * (1 + 2.0 ** -10) + 2.0 ** -126
 
 
+def gemm_magnitude(M, N, K, ta, tb, b_row):
+    """The sums of the magnitudes of run_gemm's products (seed 0)."""
+    gen = torch.Generator().manual_seed(M * 31 + N * 17 + K)
+    x = torch.randn(M, K, generator=gen) * torch.exp(torch.randn(M, 1, generator=gen))
+    w = torch.randn(N, K, generator=gen) * max(K, 1) ** -0.5
+    (A, sa), (B, sb) = quantize(x, ta, False), quantize(w, tb, not b_row)
+    return gemm_ref(A.abs(), sa, B.abs(), sb, b_row)[0]
+
+
 def check_gemm(*a, **kw):
     got, ref, bound = run_gemm(*a, **kw)
     check_close(got, ref, bound)
@@ -219,6 +228,29 @@ def test_gemm_nan_stays_in_its_row(M):
     assert got[bad].isnan().all()
     keep = [m for m in range(M) if m != bad]
     check_close(got[keep], ref[keep], bound[keep])
+
+
+@pytest.fixture
+def options():
+    yield T.tcm_set_option
+    T.tcm_set_option("fp8_config", -1)
+    T.tcm_set_option("fp8_split", 0)
+
+
+@pytest.mark.parametrize("config", [0, 1, 2, 3])
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (64, 128, 128), (257, 129, 1283), (300, 520, 1000), (130, 300, 390)])
+def test_gemm_every_tile(options, config, split, M, N, K):
+    assert options("fp8_config", config) == T.TCM_OK and options("fp8_split", split) == T.TCM_OK
+    for b_row in (False, True):
+        for ta, tb, c in ((E4M3, E4M3, torch.float32), (E5M2, E4M3, torch.bfloat16), (E4M3, E5M2, torch.float16)):
+            got, ref, bound = run_gemm(M, N, K, ta, tb, c, b_row, bias=True, accum=b_row)
+            name = (("256x256", "256x128", "128x128", "64x128")[config] if config or c != torch.float32 else "x128")
+            assert f"{name} " in T.tcm_last_plan() and f"split={min(split, blocks(K))}" in T.tcm_last_plan()
+            # 16-bit C: products cut to 2^-13 of the largest of their eight before they are added, each by less than a
+            # unit; the largest is about a third of the eight's magnitudes and the cuts average half a unit
+            mag = 0 if c == torch.float32 else 2.0 ** -12 * gemm_magnitude(M, N, K, ta, tb, b_row)
+            check_close(got, ref, bound + mag)
 
 
 def test_training_products_from_quantised_operands():
