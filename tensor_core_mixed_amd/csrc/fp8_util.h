@@ -3,6 +3,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include "lowp.h"
 #include "tcm_internal.h"
 
 namespace tcm {
@@ -81,6 +82,15 @@ __device__ __forceinline__ void store_c_any(char* p, int c_type, float v) {
                                                  : __builtin_bit_cast(unsigned short, (__bf16)v);
         __builtin_memcpy(p, &h, 2);
     }
+}
+
+// one element of C from its sum: + bias, + C's contents, ReLU, rounded to C's type
+__device__ __forceinline__ void store_epilogue(const Fp8Args& a, float v, int64_t m, int64_t n) {
+    if (a.has_bias) v += load_float<F32>((const char*)a.bias, n);
+    char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
+    if (a.accum) v += load_c_any(c, a.c_type);
+    if (a.relu) v = v > 0.f ? v : 0.f;
+    store_c_any(c, a.c_type, v);
 }
 
 }  // namespace tcm

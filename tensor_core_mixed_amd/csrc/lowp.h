@@ -67,6 +67,10 @@ int launch_fp8_tile_e5m2_e4m3(int cfg, const Fp8Args& a, void* stream);
 int launch_fp8_tile_e4m3_e5m2(int cfg, const Fp8Args& a, void* stream);
 int launch_fp8_tile_e5m2_e5m2(int cfg, const Fp8Args& a, void* stream);
 int launch_fp8_tile_sum(int cfg, const Fp8Args& a, void* stream);
+// A few rows: workgroups of kFp8SkinnyCols columns by up to kFp8SkinnyRows
+// rows (`rows`, a row block; a.tiles_m of them), a.split k ranges.
+constexpr int kFp8SkinnyCols = 16, kFp8SkinnyRows = 64;
+int launch_fp8_skinny(int rows, const Fp8Args& a, void* stream);
 
 struct RouteArgs {
     const void* x;         // [tokens][experts]
@@ -99,9 +103,9 @@ int64_t moe_generic_workspace(const MoeArgs& a);
 int launch_moe_generic(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
 
 // Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the
-// planner's choice, else a row of kFp8Tiles or kFp8Generic; and the k ranges
-// of a tile, 0 the planner's choice.
-constexpr int kFp8Generic = kNumFp8Tiles, kFp8MaxSplit = 64;
+// planner's choice, else a row of kFp8Tiles, kFp8Skinny or kFp8Generic; and
+// the k ranges of a tile, 0 the planner's choice.
+constexpr int kFp8Skinny = kNumFp8Tiles, kFp8Generic = kNumFp8Tiles + 1, kFp8MaxSplit = 64;
 struct LowpOpts {
     int fp8_config = -1, fp8_split = 0;
 };

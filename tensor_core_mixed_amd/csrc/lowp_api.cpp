@@ -117,10 +117,12 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
     const bool wide = a.c_type == C_ACC;
     const int64_t steps = scale_blocks(a.K);
     double best_t = 1e30;
+    int forced = o.fp8_config;
+    if (forced >= 0 && forced < kNumFp8Tiles && wide && !kFp8Tiles[forced].wide) forced = -1;  // cannot serve
     for (int c = 0; c < kNumFp8Tiles; ++c) {
         const Fp8Tile& t = kFp8Tiles[c];
         if (wide && !t.wide) continue;
-        if (o.fp8_config >= 0 && c != o.fp8_config && (!wide || kFp8Tiles[o.fp8_config].wide)) continue;
+        if (forced >= 0 && c != forced) continue;
         const int64_t tiles = ((a.M + t.bm - 1) / t.bm) * ((a.N + t.bn - 1) / t.bn);
         const double lone = wide ? kStep[c].lone_wide : kStep[c].lone, shared = wide ? kStep[c].shared_wide : kStep[c].shared;
         const int64_t slots = 256 * kStep[c].per_cu;
@@ -131,6 +133,19 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
             const double time = kFixed + (double)((steps + s - 1) / s) * step +
                                 (s > 1 ? kSum + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t) best_t = time, best = {c, s};
+        }
+    }
+    // Few rows: a workgroup's waves take a block each at a time, rows cost reads of A from the caches.
+    if (forced < 0 ? a.M <= kFp8SkinnyRows : forced == kFp8Skinny) {
+        static constexpr double kRound[4] = {0.9, 1.4, 1.9, 2.9};
+        const int64_t blocks_m = (a.M + kFp8SkinnyRows - 1) / kFp8SkinnyRows;
+        const int64_t wgs = blocks_m * ((a.N + kFp8SkinnyCols - 1) / kFp8SkinnyCols);
+        const double round = kRound[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
+        for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
+            if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
+            const double time = kFixed + (double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round +
+                                (s > 1 ? kSum + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            if (time < best_t) best_t = time, best = {kFp8Skinny, s};
         }
     }
     return best;
@@ -195,7 +210,10 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
         set_last_plan(text);
         return done(launch_fp8_generic(a, stream));
     }
-    const Fp8Tile& t = kFp8Tiles[pl.config];
+    const bool skinny = pl.config == kFp8Skinny;
+    const int64_t blocks_m = (M + kFp8SkinnyRows - 1) / kFp8SkinnyRows;
+    const Fp8Tile t = skinny ? Fp8Tile{(int)((M + blocks_m * 16 - 1) / (blocks_m * 16)) * 16, kFp8SkinnyCols, 1, 1, 0, true}
+                             : kFp8Tiles[pl.config];
     const int64_t tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
     if (tm * tn * pl.split >= ((int64_t)1 << 22)) return TCM_ERR_NOT_SUPPORTED;
     a.tiles_m = (int)tm;
@@ -205,13 +223,14 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
     a.split = pl.split;
     if (a.split > 1) {
         void* ws = nullptr;
-        const int st = workspace_for(stream, tm * tn * a.split * t.bm * t.bn * 4, &ws);
+        const int st = workspace_for(stream, (skinny ? M * N : tm * tn * t.bm * t.bn) * a.split * 4, &ws);
         if (st != TCM_OK) return st;
         a.ws = (float*)ws;
     }
-    snprintf(text, sizeof text, "kernel=fp8_tile tile=%dx%d tiles=%lld split=%d M=%lld N=%lld K=%lld", t.bm, t.bn,
-             (long long)(tm * tn), a.split, (long long)M, (long long)N, (long long)K);
+    snprintf(text, sizeof text, "kernel=fp8_%s tile=%dx%d tiles=%lld split=%d M=%lld N=%lld K=%lld", skinny ? "skinny" : "tile",
+             t.bm, t.bn, (long long)(tm * tn), a.split, (long long)M, (long long)N, (long long)K);
     set_last_plan(text);
+    if (skinny) return done(launch_fp8_skinny(t.bm, a, stream));
     const auto launch = a.a_e5m2 ? (a.b_e5m2 ? launch_fp8_tile_e5m2_e5m2 : launch_fp8_tile_e5m2_e4m3)
                                  : (a.b_e5m2 ? launch_fp8_tile_e4m3_e5m2 : launch_fp8_tile_e4m3_e4m3);
     if (launch(pl.config, a, stream) != 0) return TCM_ERR_HIP;

@@ -253,6 +253,16 @@ def test_gemm_every_tile(options, config, split, M, N, K):
             check_close(got, ref, bound + mag)
 
 
+@pytest.mark.parametrize("split", [1, 2, 5])
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (16, 33, 1024), (17, 50, 2050), (48, 128, 777), (64, 300, 1664), (150, 40, 1300)])
+def test_gemm_few_rows_kernel(options, split, M, N, K):
+    assert options("fp8_config", 4) == T.TCM_OK and options("fp8_split", split) == T.TCM_OK
+    for b_row in (False, True):
+        for ta, tb, c in ((E4M3, E4M3, torch.float32), (E5M2, E4M3, torch.bfloat16), (E4M3, E5M2, torch.float16), (E5M2, E5M2, torch.float32)):
+            check_gemm(M, N, K, ta, tb, c, b_row, bias=True, relu=M == 17, accum=b_row)
+            assert "fp8_skinny" in T.tcm_last_plan()
+
+
 def test_training_products_from_quantised_operands():
     """y, dx and dW of a linear layer from one quantisation each of x, W and dy, against the same products in 64 bits."""
     gen = torch.Generator().manual_seed(11)
