@@ -97,9 +97,15 @@ struct MoeArgs {
     void* out;             // [tokens][hidden], x's type
     int64_t ldo;
     int tokens, hidden, inter, experts, topk;
-    void* ws;              // moe_workspace_bytes of scratch
+    void* ws;              // h, the products between the matrices: [pair][inter] binary32
+    // the tiled kernels
+    float* y;              // [pair][hidden]
+    unsigned* hmax;        // float16 weights: |h|'s largest of each 16, [pair][inter / 16]
 };
-int64_t moe_generic_workspace(const MoeArgs& a);
+// Tiled kernels: rows of x, w1 and w2 at multiples of 4 bytes, at most
+// kMoePairs pairs a call.
+constexpr int kMoePairs = 1024;
+int launch_moe_tile(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
 int launch_moe_generic(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
 
 // Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the

@@ -314,12 +314,23 @@ int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int
     a.experts = (int)experts;
     a.topk = work ? (int)topk : 0;
     char text[200];
-    // a launch counts its threads in 32 bits: tokens in chunks of 2^24 waves at most
+    // whole words in every row: the tiled kernels, in calls of kMoePairs pairs at most
+    const int64_t per_word = w8 ? 4 : 2;
+    const auto words = [](const void* p) { return ((uintptr_t)p & 3) == 0; };
+    const bool tiled = work && topk <= kMoePairs && words(x) && words(w1) && words(w2) && ldx % 2 == 0 && hidden % per_word == 0 &&
+                       inter % per_word == 0 && experts * std::max(hidden, inter) < ((int64_t)1 << 26);
+    // (a launch counts its threads in 32 bits: the others take 2^25 waves at most)
     const int64_t per_token = std::max<int64_t>(hidden, work ? topk * inter : 0);
-    const int64_t chunk = std::min<int64_t>(((int64_t)1 << 25) / per_token, tokens);
+    const int64_t chunk = std::min<int64_t>(tiled ? kMoePairs / topk : ((int64_t)1 << 25) / per_token, tokens);
     if (chunk == 0) return TCM_ERR_NOT_SUPPORTED;
-    snprintf(text, sizeof text, "kernel=moe_generic tokens=%lld hidden=%lld inter=%lld experts=%lld topk=%lld dtype=%d e4m3=%d",
-             (long long)tokens, (long long)hidden, (long long)inter, (long long)experts, (long long)topk, t, (int)w8);
+    const int64_t h_bytes = (chunk * a.topk * inter * 4 + 15) & ~(int64_t)15, y_bytes = (chunk * a.topk * hidden * 4 + 15) & ~(int64_t)15;
+    const int st = workspace_for(stream, std::max<int64_t>(tiled ? h_bytes + y_bytes + chunk * topk * ((inter + 15) / 16) * 4 : h_bytes, 4), &a.ws);
+    if (st != TCM_OK) return st;
+    a.y = (float*)((char*)a.ws + h_bytes);
+    a.hmax = (unsigned*)((char*)a.ws + h_bytes + y_bytes);
+    snprintf(text, sizeof text, "kernel=moe_%s tokens=%lld hidden=%lld inter=%lld experts=%lld topk=%lld dtype=%d e4m3=%d",
+             tiled ? "tile" : "generic", (long long)tokens, (long long)hidden, (long long)inter, (long long)experts, (long long)topk, t,
+             (int)w8);
     set_last_plan(text);
     for (int64_t t0 = 0; t0 < tokens; t0 += chunk) {
         a.tokens = (int)std::min(chunk, tokens - t0);
@@ -327,9 +338,7 @@ int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int
         a.ids = ids + t0 * a.topk;
         a.weights = weights + t0 * a.topk;
         a.out = (char*)out + t0 * ldo * 2;
-        const int st = workspace_for(stream, std::max<int64_t>(moe_generic_workspace(a), 4), &a.ws);
-        if (st != TCM_OK) return st;
-        if (launch_moe_generic(t, w8, a, stream) != 0) return TCM_ERR_HIP;
+        if ((tiled ? launch_moe_tile : launch_moe_generic)(t, w8, a, stream) != 0) return TCM_ERR_HIP;
     }
     return TCM_OK;
 }

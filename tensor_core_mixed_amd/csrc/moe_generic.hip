@@ -89,8 +89,6 @@ int launch(const MoeArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int64_t moe_generic_workspace(const MoeArgs& a) { return (int64_t)a.tokens * a.topk * a.inter * 4; }
-
 int launch_moe_generic(int x_type, bool w_e4m3, const MoeArgs& a, void* stream) {
     hipStream_t s = (hipStream_t)stream;
     if (x_type == F16) return w_e4m3 ? launch<F16, true>(a, s) : launch<F16, false>(a, s);
