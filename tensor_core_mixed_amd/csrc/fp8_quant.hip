@@ -7,22 +7,30 @@
 // lies, transposed (blocks then run down x's columns), or both from one read.
 //
 // Every q is the nearest value to the exact quotient, ties to even.  With
-// r = 1/s to an ulp, x r (1 - 2^-20) and x r (1 + 2^-20) enclose the exact
-// quotient; where both round to the same 8-bit value (all but about one
-// element in 10^5 of ordinary data) that is the answer, for two
-// multiplications and a packed conversion an element.  Where they differ, a
-// middle m of two neighbouring values lies between them, and |x| is compared
-// with |m| s in binary64, which holds that product exactly.
+// r = 1/s to an ulp, x r (1 - 2^-21) and x r (1 + 2^-21) enclose the exact
+// quotient; where both round to the same 8-bit value that is the answer, for
+// two multiplications and a packed conversion an element.  Where they differ,
+// a middle m of two neighbouring values lies between them, and the sign of
+// |x| - |m| s, which one fused multiply-add gives exactly, settles it.
+//
+// 32-bit inputs meet such an element once in 10^5, but of 16-bit ones x L /
+// amax is often a middle exactly (both have few bits), and is otherwise at
+// least 2^-16 away from one.  Where s is amax / L rounded up, x / s then lies
+// below that middle, and the lower factor alone gives every answer; where it
+// is rounded down the upper; only blocks whose s is exact have ties to settle.
 //
 // NaN and infinity follow the formula: a block that holds a NaN has a NaN
 // scale and all q NaN; one with an infinity (and no NaN) has an infinite
 // scale, finite x become 0 and the infinities NaN.
 //
-// A workgroup takes one 128 x 128 tile, a thread an 8 x 8 block of it: 16
-// lanes read 128 consecutive values of a row (16 bytes a lane for 16-bit
-// types), and a thread holds 8 consecutive values in both directions, so the
-// bytes of either output pack in registers.  Transposed bytes pass through
-// 16 KiB of LDS to be stored 128 bytes of a line at a time.
+// Tile kernel: a workgroup takes one 128 x 128 tile, a thread an 8 x 8 block
+// of it: 16 lanes read 128 consecutive values of a row (16 bytes a lane for
+// 16-bit types), and a thread holds 8 consecutive values in both directions,
+// so the bytes of either output pack in registers.  A lane works out one
+// row's factors and the 16 lanes of the row share them; a column's go through
+// LDS.  Transposed bytes pass through 16 KiB of LDS to be stored 128 bytes of
+// a line at a time.  Row kernel: row blocks as they lie need no tile; 16
+// lanes take a block, and short matrices fill more of the chip.
 #include <hip/hip_runtime.h>
 
 #include "fp8_util.h"
@@ -34,6 +42,7 @@ namespace quant {
 constexpr int kThreads = 256;
 typedef unsigned u2_t __attribute__((ext_vector_type(2)));
 typedef unsigned u4_t __attribute__((ext_vector_type(4)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
 
 // one step of a maximum over 16 lanes: with the value of the lane ROR places
 // away in the row of 16
@@ -49,10 +58,16 @@ __device__ __forceinline__ unsigned umax(unsigned a, unsigned b) { return a > b 
 
 // |x|'s bits: unsigned order is magnitude order, NaN above infinity
 __device__ __forceinline__ unsigned mag(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
+// a maximum that keeps a NaN
+__device__ __forceinline__ float max_abs(float m, float v) { return __builtin_elementwise_maximum(m, __builtin_fabsf(v)); }
 
+// amax / L, correctly rounded: the product with 1/L corrected by its
+// remainder, which a fused multiply-add gives exactly.
 template <bool E5M2>
 __device__ __forceinline__ float scale_of(unsigned amax) {
-    const float s = __builtin_bit_cast(float, amax) / (E5M2 ? kE5M2Max : kE4M3Max);
+    constexpr float L = E5M2 ? kE5M2Max : kE4M3Max;
+    const float x = __builtin_bit_cast(float, amax), q = x * (1.f / L);
+    const float s = amax == 0x7f800000u ? x : __builtin_fmaf(__builtin_fmaf(-L, q, x), 1.f / L, q);
     return s < kScaleMin ? kScaleMin : s;  // a NaN stays
 }
 
@@ -60,30 +75,67 @@ __device__ __forceinline__ float scale_of(unsigned amax) {
 struct Recip {
     float lo, hi;
 };
-__device__ __forceinline__ Recip recip_of(float s) {
+template <int XT, bool E5M2>
+__device__ __forceinline__ Recip recip_of(float s, unsigned amax) {
     const float r = __builtin_amdgcn_rcpf(s);
-    return Recip{r * (1.f - 0x1p-20f), r * (1.f + 0x1p-20f)};
+    Recip f{r * (1.f - 0x1p-21f), r * (1.f + 0x1p-21f)};
+    if constexpr (XT != F32) {
+        const float rest = __builtin_fmaf(-(E5M2 ? kE5M2Max : kE4M3Max), s, __builtin_bit_cast(float, amax));
+        const bool exact = s <= kScaleMin;  // (the least scale: a power of two)
+        if (rest > 0.f && !exact) f.lo = f.hi;
+        if (rest < 0.f && !exact) f.hi = f.lo;
+    }
+    return f;
 }
 
-// a byte of which the enclosing quotients disagree
-template <bool E5M2>
-__device__ __forceinline__ unsigned settle(unsigned c0, unsigned c1, float x, float s) {
-    if (c0 == c1) return c0;
-    const double m = 0.5 * ((double)fp8_decode<E5M2>(c0) + (double)fp8_decode<E5M2>(c1));
-    const double d = fabs((double)x) - fabs(m) * (double)s;
-    return d > 0 ? c1 : (d < 0 ? c0 : ((c0 & 1) ? c1 : c0));
-}
-template <bool E5M2>
-__device__ __forceinline__ unsigned quant4(const float (&x)[4], const float (&s)[4], const Recip (&r)[4]) {
-    unsigned lo = fp8_encode4<E5M2>(x[0] * r[0].lo, x[1] * r[1].lo, x[2] * r[2].lo, x[3] * r[3].lo);
-    const unsigned hi = fp8_encode4<E5M2>(x[0] * r[0].hi, x[1] * r[1].hi, x[2] * r[2].hi, x[3] * r[3].hi);
-    if (lo != hi) {
-        unsigned w = 0;
+// eight values' bytes; scale() is asked for s where the factors disagree
+template <bool E5M2, class S>
+__device__ __forceinline__ u2_t quant8(const float (&x)[8], float lo, float hi, S scale) {
+    u2_t w, u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w |= settle<E5M2>((lo >> (8 * i)) & 255, (hi >> (8 * i)) & 255, x[i], s[i]) << (8 * i);
-        lo = w;
+    for (int h = 0; h < 2; ++h) {
+        const float* v = x + 4 * h;
+        w[h] = fp8_encode4<E5M2>(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo);
+        u[h] = fp8_encode4<E5M2>(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi);
     }
-    return lo;
+    if (__ballot(((w[0] ^ u[0]) | (w[1] ^ u[1])) != 0)) {
+        const float s = scale();
+        const float up = s < 0x1p-90f ? 0x1p64f : 1.f;  // (keeps the difference above the least binary32 value)
+        const float half = 0.5f * (s * up);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            unsigned o = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned c0 = (w[h] >> (8 * i)) & 255, c1 = (u[h] >> (8 * i)) & 255;
+                const float m2 = fp8_decode<E5M2>(c0) + fp8_decode<E5M2>(c1);
+                const float d = __builtin_fmaf(-__builtin_fabsf(m2), half, __builtin_fabsf(x[4 * h + i] * up));
+                const unsigned even = (c0 & 1) ? c1 : c0;
+                o |= (d > 0.f ? c1 : (d < 0.f ? c0 : even)) << (8 * i);
+            }
+            w[h] = o;
+        }
+    }
+    return w;
+}
+
+// eight consecutive values of a row from p on, of which n exist
+template <int XT>
+__device__ __forceinline__ void load8(float (&v)[8], const char* p, int64_t n) {
+    constexpr int ES = XT == F32 ? 4 : 2;
+    if (n >= 8) {
+        unsigned w[2 * ES];
+        __builtin_memcpy(w, p, 8 * ES);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (XT == F32) v[j] = __builtin_bit_cast(float, w[j]);
+            else if constexpr (XT == BF16) v[j] = __builtin_bit_cast(float, (j & 1) ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+            else v[j] = (float)__builtin_bit_cast(_Float16, (unsigned short)((j & 1) ? w[j >> 1] >> 16 : w[j >> 1]));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? load_float<XT>(p, j) : 0.f;
+    }
 }
 
 // bytes [0, n) of two words, n <= 8, to any address
@@ -97,119 +149,124 @@ __device__ __forceinline__ void store_bytes8(unsigned char* p, u2_t w, int64_t n
     }
 }
 
+// lane I of the row of 16 to all of them
+template <int I>
+__device__ __forceinline__ float row_lane(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + I, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_lane(float v, int i) {  // (i a constant once unrolled)
+    switch (i) {
+    case 0: return row_lane<0>(v);
+    case 1: return row_lane<1>(v);
+    case 2: return row_lane<2>(v);
+    case 3: return row_lane<3>(v);
+    case 4: return row_lane<4>(v);
+    case 5: return row_lane<5>(v);
+    case 6: return row_lane<6>(v);
+    default: return row_lane<7>(v);
+    }
+}
+
 template <int XT, bool E5M2, bool TILE>
-__global__ __launch_bounds__(kThreads) void quant_kernel(QuantArgs a) {
-    __shared__ u2_t tr[128 * 16];        // transposed bytes: [column][8-byte piece ^ (column / 8)]
-    __shared__ unsigned part[4][128];    // each wave's column maxima; row 0 the tile's with TILE
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void quant_tile_kernel(QuantArgs a) {
+    constexpr int ES = XT == F32 ? 4 : 2;
+    __shared__ u2_t tr[128 * 16];        // transposed bytes: [column][8-byte piece ^ (column / 8)]; before them
+                                         // each row group's column maxima, [row group][column]
+    __shared__ float fs[128], flo[128], fhi[128];  // the columns' scales and factors
+    __shared__ unsigned part[4];
     const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15, wave = tid >> 6;
     const int64_t bc = blockIdx.x, br = blockIdx.y;
     const int64_t row0 = br * 128 + 8 * rg, col0 = bc * 128 + 8 * cg;
 
     float v[8][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool in = row0 + i < a.rows;
-        constexpr int ES = XT == F32 ? 4 : 2;
-        const char* p = (const char*)a.x + ((row0 + i) * a.ldx + col0) * ES;
-        if (in && col0 + 8 <= a.cols) {
-            unsigned w[2 * ES];
-            __builtin_memcpy(w, p, 8 * ES);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (XT == F32) v[i][j] = __builtin_bit_cast(float, w[j]);
-                else if constexpr (XT == BF16) v[i][j] = __builtin_bit_cast(float, (j & 1) ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
-                else v[i][j] = (float)__builtin_bit_cast(_Float16, (unsigned short)((j & 1) ? w[j >> 1] >> 16 : w[j >> 1]));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = in && col0 + j < a.cols ? load_float<XT>(p, j) : 0.f;
-        }
-    }
+    for (int i = 0; i < 8; ++i)
+        load8<XT>(v[i], (const char*)a.x + ((row0 + i) * a.ldx + col0) * ES, row0 + i < a.rows ? a.cols - col0 : 0);
 
-    unsigned rmax[8], cmax[8];
+    float rmax[8], cmax[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rmax[i] = cmax[i] = 0;
+    for (int i = 0; i < 8; ++i) rmax[i] = cmax[i] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const unsigned m = mag(v[i][j]);
-            rmax[i] = umax(rmax[i], m);
-            cmax[j] = umax(cmax[j], m);
+            if (TILE || a.q) rmax[i] = max_abs(rmax[i], v[i][j]);
+            if (!TILE) cmax[j] = max_abs(cmax[j], v[i][j]);
         }
 
     float s_tile = 0.f;
+    Recip r_tile{};
     if constexpr (TILE) {
         unsigned m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = umax(m, rmax[i]);
+        for (int i = 0; i < 8; ++i) m = umax(m, mag(rmax[i]));
         m = max16(m);
         m = umax(m, __shfl_xor(m, 16));
         m = umax(m, __shfl_xor(m, 32));
-        if ((tid & 63) == 0) part[0][wave] = m;
+        if ((tid & 63) == 0) part[wave] = m;
         __syncthreads();
-        m = umax(umax(part[0][0], part[0][1]), umax(part[0][2], part[0][3]));
+        m = umax(umax(part[0], part[1]), umax(part[2], part[3]));
         s_tile = scale_of<E5M2>(m);
+        r_tile = recip_of<XT, E5M2>(s_tile, m);
         if (tid == 0) {
             if (a.q) a.s[br * a.lds + bc] = s_tile;
             if (a.qt) a.st[bc * a.ldst + br] = s_tile;
         }
+    } else if (a.qt) {
+        f4_t* o = (f4_t*)tr + rg * 32 + 2 * cg;
+        o[0] = f4_t{cmax[0], cmax[1], cmax[2], cmax[3]};
+        o[1] = f4_t{cmax[4], cmax[5], cmax[6], cmax[7]};
+        __syncthreads();
+        if (tid < 128) {
+            float m = 0.f;
+#pragma unroll
+            for (int g = 0; g < 16; ++g) m = max_abs(m, ((const float*)tr)[g * 128 + tid]);
+            const float s = scale_of<E5M2>(mag(m));
+            const Recip r = recip_of<XT, E5M2>(s, mag(m));
+            fs[tid] = s;
+            flo[tid] = r.lo;
+            fhi[tid] = r.hi;
+            if (bc * 128 + tid < a.cols) a.st[br * a.ldst + bc * 128 + tid] = s;
+        }
+        __syncthreads();
     }
 
     if (a.q) {
-        float keep = 0.f;
+        // lane i of a row of 16 (and i + 8) works out row i's scale and factors
+        float s = s_tile;
+        Recip r = r_tile;
+        if constexpr (!TILE) {
+            unsigned m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const unsigned x = max16(mag(rmax[i]));
+                m = (cg & 7) == i ? x : m;
+            }
+            s = scale_of<E5M2>(m);
+            r = recip_of<XT, E5M2>(s, m);
+            if (cg < 8 && row0 + cg < a.rows) a.s[bc * a.lds + row0 + cg] = s;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float s = TILE ? s_tile : scale_of<E5M2>(max16(rmax[i]));
-            const Recip r = recip_of(s);
-            if (cg == i) keep = s;
-            u2_t w;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[h] = quant4<E5M2>({v[i][4 * h], v[i][4 * h + 1], v[i][4 * h + 2], v[i][4 * h + 3]}, {s, s, s, s}, {r, r, r, r});
+            const float lo = TILE ? r.lo : row_lane(r.lo, i), hi = TILE ? r.hi : row_lane(r.hi, i);
+            const u2_t w = quant8<E5M2>(v[i], lo, hi, [&] { return TILE ? s : row_lane(s, i); });
             if (row0 + i < a.rows) store_bytes8(a.q + (row0 + i) * a.ldq + col0, w, a.cols - col0);
         }
-        if (!TILE && cg < 8 && row0 + cg < a.rows) a.s[bc * a.lds + row0 + cg] = keep;
     }
     if (!a.qt) return;
 
-    float sc[8];
-    Recip rc[8];
-    if constexpr (!TILE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            cmax[j] = umax(cmax[j], __shfl_xor(cmax[j], 16));
-            cmax[j] = umax(cmax[j], __shfl_xor(cmax[j], 32));
-        }
-        if ((tid & 63) < 16) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) part[wave][8 * cg + j] = cmax[j];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = 8 * cg + j;
-            sc[j] = scale_of<E5M2>(umax(umax(part[0][c], part[1][c]), umax(part[2][c], part[3][c])));
-        }
-        if (rg == 0) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col0 + j < a.cols) a.st[br * a.ldst + col0 + j] = sc[j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sc[j] = s_tile;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) rc[j] = recip_of(sc[j]);
+    float lo[8], hi[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        u2_t w;
+        lo[j] = TILE ? r_tile.lo : flo[8 * cg + j];
+        hi[j] = TILE ? r_tile.hi : fhi[8 * cg + j];
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[h] = quant4<E5M2>({v[4 * h][j], v[4 * h + 1][j], v[4 * h + 2][j], v[4 * h + 3][j]}, {sc[j], sc[j], sc[j], sc[j]},
-                                {rc[j], rc[j], rc[j], rc[j]});
-        tr[(8 * cg + j) * 16 + (rg ^ cg)] = w;
+    for (int j = 0; j < 8; ++j) {
+        float c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = v[i][j];
+        tr[(8 * cg + j) * 16 + (rg ^ cg)] = quant8<E5M2>(c, lo[j], hi[j], [&] { return TILE ? s_tile : fs[8 * cg + j]; });
     }
     __syncthreads();
 #pragma unroll
@@ -230,26 +287,53 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantArgs a) {
     }
 }
 
+// Row blocks as they lie: 16 lanes a block, the blocks of 16 rows a workgroup.
+template <int XT, bool E5M2>
+__global__ __launch_bounds__(kThreads) void quant_row_kernel(QuantArgs a) {
+    constexpr int ES = XT == F32 ? 4 : 2;
+    const int cg = threadIdx.x & 15;
+    const int64_t bc = blockIdx.x, row = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4), col0 = bc * 128 + 8 * cg;
+    const char* p = (const char*)a.x + (row * a.ldx + col0) * ES;
+    const int64_t n = row < a.rows ? a.cols - col0 : 0;
+    float v[8];
+    load8<XT>(v, p, n);
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max_abs(m, v[j]);
+    const unsigned amax = max16(mag(m));
+    const float s = scale_of<E5M2>(amax);
+    const Recip r = recip_of<XT, E5M2>(s, amax);
+    const u2_t w = quant8<E5M2>(v, r.lo, r.hi, [&] { return s; });
+    if (n <= 0) return;
+    if (cg == 0) a.s[bc * a.lds + row] = s;
+    store_bytes8(a.q + row * a.ldq + col0, w, n);
+}
+
 template <int XT>
 int launch_x(bool e5m2, bool tile, const QuantArgs& a, hipStream_t s) {
-    const int64_t nc = scale_blocks(a.cols), nr = scale_blocks(a.rows);
-    // the grid's y extent holds 65535 tiles: longer matrices go in bands
+    const bool rows_only = !tile && !a.qt;
+    const int64_t high = rows_only ? 16 : 128;
+    const int64_t nc = scale_blocks(a.cols), nr = (a.rows + high - 1) / high;
+    // the grid's y extent holds 65535 workgroups: longer matrices go in bands
     for (int64_t b = 0; b < nr; b += 65535) {
         QuantArgs e = a;
-        const int64_t r0 = b * 128;
+        const int64_t r0 = b * high;
         e.rows = a.rows - r0;
         e.x = (const char*)a.x + r0 * a.ldx * (XT == F32 ? 4 : 2);
         if (a.q) e.q = a.q + r0 * a.ldq, e.s = a.s + (tile ? b * a.lds : r0);
         if (a.qt) e.qt = a.qt + r0, e.st = a.st + (tile ? b : b * a.ldst);
         const int64_t n = nr - b < 65535 ? nr - b : 65535;
-        if (n * 128 < e.rows) e.rows = n * 128;
+        if (n * high < e.rows) e.rows = n * high;
         const dim3 grid((unsigned)nc, (unsigned)n);
-        if (e5m2) {
-            if (tile) hipLaunchKernelGGL((quant_kernel<XT, true, true>), grid, dim3(kThreads), 0, s, e);
-            else hipLaunchKernelGGL((quant_kernel<XT, true, false>), grid, dim3(kThreads), 0, s, e);
+        if (rows_only) {
+            if (e5m2) hipLaunchKernelGGL((quant_row_kernel<XT, true>), grid, dim3(kThreads), 0, s, e);
+            else hipLaunchKernelGGL((quant_row_kernel<XT, false>), grid, dim3(kThreads), 0, s, e);
+        } else if (e5m2) {
+            if (tile) hipLaunchKernelGGL((quant_tile_kernel<XT, true, true>), grid, dim3(kThreads), 0, s, e);
+            else hipLaunchKernelGGL((quant_tile_kernel<XT, true, false>), grid, dim3(kThreads), 0, s, e);
         } else {
-            if (tile) hipLaunchKernelGGL((quant_kernel<XT, false, true>), grid, dim3(kThreads), 0, s, e);
-            else hipLaunchKernelGGL((quant_kernel<XT, false, false>), grid, dim3(kThreads), 0, s, e);
+            if (tile) hipLaunchKernelGGL((quant_tile_kernel<XT, false, true>), grid, dim3(kThreads), 0, s, e);
+            else hipLaunchKernelGGL((quant_tile_kernel<XT, false, false>), grid, dim3(kThreads), 0, s, e);
         }
     }
     return (int)hipGetLastError();
