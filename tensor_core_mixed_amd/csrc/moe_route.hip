@@ -6,13 +6,18 @@
 //     weight = score[id] * scale, or with norm score[id] / (sum over ids of score) * scale.
 //
 // Both scores rise with x, so without a bias the logits order the experts
-// exactly.  With a bias the keys are formed in binary64: near ones would
-// change places in 32 bits.  A sum of zero (a row of -inf) gives weights of
-// zero; a NaN key ranks above every number.
+// exactly.  With a bias the keys count in binary64: near ones would change
+// places in 32 bits.  A sum of zero (a row of -inf) gives weights of zero; a
+// NaN key ranks above every number.
 //
-// One wave takes one token, expert e on lane e % 64; the topk passes each
-// take the wave's largest remaining key, compared as order-preserving
-// integers.
+// One wave takes one token, expert e on lane e % 64.  Each pass takes the
+// wave's largest remaining key, as order-preserving 32-bit integers, by a
+// maximum over the lanes on the vector ALU, and the first expert that holds
+// it; lane j keeps choice j and works out its weight at the end.  Keys with a
+// bias are formed in binary32 first, off by less than half kSlack of the largest
+// score and of the key: a token two of whose topk + 1 first keys lie closer
+// than that is routed again by the binary64 passes, as is one with a NaN or a
+// +inf or whose logits are all -inf.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -32,11 +37,122 @@ __device__ __forceinline__ uint64_t ordered(double v) {
     return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
+__device__ __forceinline__ unsigned ordered(float v) {  // (v is no NaN)
+    const unsigned b = __builtin_bit_cast(unsigned, v + 0.f);
+    return (b >> 31) ? ~b : b | (1u << 31);
+}
+__device__ __forceinline__ float unordered(unsigned k) { return __builtin_bit_cast(float, (k >> 31) ? k & 0x7fffffffu : ~k); }
+
+template <int CTRL>
+__device__ __forceinline__ unsigned max_step(unsigned v) {
+    const unsigned o = (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+    return v > o ? v : o;
+}
+// the largest over the wave, uniform: rows of 16 (shifts by 1, 2, 4, 8), then their last lanes handed on
+__device__ __forceinline__ unsigned wave_max(unsigned v) {
+    v = max_step<0x118>(max_step<0x114>(max_step<0x112>(max_step<0x111>(v))));
+    v = max_step<0x143>(max_step<0x142>(v));
+    return (unsigned)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL>
+__device__ __forceinline__ float add_step(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_step<0x118>(add_step<0x114>(add_step<0x112>(add_step<0x111>(v))));
+    v = add_step<0x143>(add_step<0x142>(v));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Twice the error of a binary32 key, as a share of the largest score and of
+// |key|.  Of the score: the exponential's argument (|x| e^-|x| / ln 2 steps of
+// 2^-24 at most, under 1), its value, the sum (NPL + 5 additions in softmax),
+// the quotient and the product come to NPL + 11 steps of 2^-24; of the key:
+// the bias's addition, one.
+template <int NPL>
+constexpr float kSlack = NPL > 4 ? 0x1p-18f : 0x1p-19f;
+
+// One token in binary32; false where the binary64 passes have to take it.
 template <int XT, int NPL, bool BIAS>
-__global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    if (t >= a.tokens) return;
+__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int lane) {
+    const char* row = (const char*)a.x + t * a.ldx * (XT == F32 ? 4 : 2);
+    float x[NPL];
+    unsigned key[NPL];
+    float mx = -INFINITY;
+    bool odd = false;  // a NaN
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = i * 64 + lane;
+        x[i] = e < a.experts ? load_float<XT>(row, e) : -INFINITY;
+        odd |= x[i] != x[i];
+        mx = x[i] > mx ? x[i] : mx;
+    }
+    if (__ballot(odd)) return false;
+    mx = unordered(wave_max(ordered(mx)));
+    if (!(mx > -INFINITY && mx < INFINITY)) return false;
+    float sum = 0.f;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) sum += __expf(x[i] - mx);
+        sum = wave_sum(sum);
+    }
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = i * 64 + lane;
+        float k = x[i];
+        if constexpr (BIAS) {
+            const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-x[i])) : __expf(x[i] - mx) * inv;
+            k = s + (e < a.experts ? load_float<F32>((const char*)a.bias, e) : 0.f);
+            odd |= !(k > -INFINITY && k < INFINITY);
+        }
+        key[i] = e < a.experts ? ordered(k) : 0;
+    }
+    if constexpr (BIAS) {
+        if (__ballot(odd)) return false;
+    }
+    const float slack = a.sigmoid ? kSlack<NPL> : kSlack<NPL> * inv;  // (of the largest score)
+    const int passes = BIAS ? min(a.topk + 1, a.experts) : a.topk;
+    int my_id = 0;
+    float my_x = 0.f, last = INFINITY;
+    for (int j = 0; j < passes; ++j) {
+        unsigned m = key[0];
+#pragma unroll
+        for (int i = 1; i < NPL; ++i) m = key[i] > m ? key[i] : m;
+        m = wave_max(m);
+        if constexpr (BIAS) {
+            const float k = unordered(m);
+            if (last - k <= slack + kSlack<NPL> * (k < 0.f ? -k : k)) return false;
+            last = k;
+        }
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            if (found) continue;
+            const unsigned long long h = __ballot(key[i] == m);
+            if (h == 0) continue;
+            found = true;
+            const int l = __builtin_ctzll(h);
+            if (lane == l) key[i] = 0;
+            const float xv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x[i]), l));
+            if (lane == j) my_id = i * 64 + l, my_x = xv;
+        }
+    }
+    float w = 0.f;
+    if (lane < a.topk) w = a.sigmoid ? 1.f / (1.f + expf(-my_x)) : expf(my_x - mx) * inv;
+    if (a.norm) {
+        const float total = wave_sum(w);
+        w = total == 0.f ? 0.f : w / total;
+    }
+    if (lane < a.topk) {
+        a.ids[t * a.topk + lane] = my_id;
+        a.weights[t * a.topk + lane] = w * a.scale;
+    }
+    return true;
+}
+
+template <int XT, int NPL, bool BIAS>
+__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int lane) {
     const char* row = (const char*)a.x + t * a.ldx * (XT == F32 ? 4 : 2);
     double sc[NPL];  // this lane's scores
     uint64_t key[NPL];
@@ -71,27 +187,31 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
         const int e = i * 64 + lane;
         key[i] = e >= a.experts ? 0 : ordered(BIAS ? sc[i] + (double)load_float<F32>((const char*)a.bias, e) : (double)x[i]);
     }
-    int my_id = 0;       // lane j keeps choice j
+    int my_id = 0;  // lane j keeps choice j
     double my_score = 0, total = 0;
-    unsigned taken = 0;  // of this lane's values
     for (int j = 0; j < a.topk; ++j) {
-        uint64_t best = 0;
-        int be = 1 << 30;
-        double bs = 0;
+        // the largest upper half, then among its holders the largest lower half
+        unsigned hi = 0, lo = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) hi = max(hi, (unsigned)(key[i] >> 32));
+        hi = wave_max(hi);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) lo = (unsigned)(key[i] >> 32) == hi ? max(lo, (unsigned)key[i]) : lo;
+        lo = wave_max(lo);
+        const uint64_t m = (uint64_t)hi << 32 | lo;
+        bool found = false;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            const int e = i * 64 + lane;
-            if (e < a.experts && !((taken >> i) & 1) && (be == 1 << 30 || key[i] > best)) best = key[i], be = e, bs = sc[i];
+            if (found) continue;
+            const unsigned long long h = __ballot(key[i] == m);
+            if (h == 0) continue;
+            found = true;
+            const int l = __builtin_ctzll(h);
+            if (lane == l) key[i] = 0;
+            const double s = __shfl(sc[i], l);
+            if (lane == j) my_id = i * 64 + l, my_score = s;
+            total += s;
         }
-        for (int o = 32; o; o >>= 1) {
-            const uint64_t ok = __shfl_xor(best, o);
-            const int oe = __shfl_xor(be, o);
-            const double os = __shfl_xor(bs, o);
-            if (oe != 1 << 30 && (be == 1 << 30 || ok > best || (ok == best && oe < be))) best = ok, be = oe, bs = os;
-        }
-        if ((be & 63) == lane) taken |= 1u << (be >> 6);
-        if (j == lane) my_id = be, my_score = bs;
-        total += bs;
     }
     if (lane < a.topk) {
         double w = my_score;
@@ -99,6 +219,14 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
         a.ids[t * a.topk + lane] = my_id;
         a.weights[t * a.topk + lane] = (float)(w * (double)a.scale);
     }
+}
+
+template <int XT, int NPL, bool BIAS>
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (t >= a.tokens) return;
+    if (!route_fast<XT, NPL, BIAS>(a, t, lane)) route_exact<XT, NPL, BIAS>(a, t, lane);
 }
 
 template <int XT, int NPL>
