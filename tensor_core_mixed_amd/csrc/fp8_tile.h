@@ -145,106 +145,125 @@ struct Tile {
     static_assert(BN / WN == 64, "a wave covers 64 columns");
     static constexpr int GM = FM >= 4 ? 2 : 1, NG = FM / GM;        // row tiles taken together, groups a K-step
     static_assert(FM % (2 * GM) == 0, "a step starts with the first of the two fragment buffers");
-    // waves 0-3 of eight copy the operands and waves 4-7 the scales; of four every wave copies its share of both
-    static constexpr int NWC = 4;
     static_assert(NW == 8 || NW == 4, "");
-    static constexpr int IA = BM / (8 * NWC), IB = BN / (8 * NWC);
+    static constexpr int IA = BM / (8 * NW), IB = BN / (8 * NW);
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + 1024;
     static constexpr int STAGE = SB_OFF + 1024;
     static constexpr int LDS = NST * STAGE;
     static_assert(LDS <= 160 * 1024 && BM <= 256 && BN <= 256, "");
 
-    // rows of A are read 16 at a time at one chunk, rows of B four by four at a distance of 16
-    __device__ __forceinline__ static int swz_a(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+    // Row i of the 16 that a fragment read takes is row i of A's tile, and of B's 16 * (i / 4) + 4 * tile + i % 4; both
+    // swizzles are i / 2 % 8: any sixteen lanes that the LDS serves at once (0-3, 12-15, 20-27 and their complements,
+    // by the counters) then fall on distinct banks.  (With i % 8 ^ i / 8 for A every read of A took twice its time.)
+    __device__ __forceinline__ static int swz_a(int r) { return (r >> 1) & 7; }
     __device__ __forceinline__ static int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 4) & 3) << 1; }
 
-    // this lane's offsets in the copies of a step, and where the next step to copy begins
+    // A wave's copies of a step: IA of A, IB of B, and of the scales one (eight waves: 0-3 A's and 4-7 B's) or two.
+    static constexpr int NS = NW == 4 ? 2 : 1, OPS = IA + IB + NS;
+    // this lane's offsets in them, and where the next step to copy begins
     struct Dma {
-        unsigned a_off, b_off[2], sa_off, sb_off;
+        unsigned a_off, b_off[2], s_off[NS];
         int a_k, b_k[2];
         const unsigned char *pa, *pb;
-        const float *psa, *psb;
-        int64_t sa_step, sb_step;  // floats
+        const float* ps[NS];
+        int64_t s_step[NS];  // floats
+        int s_lds[NS];
         unsigned a_hop, b_hop;
-        int a_range, b_range, k_left;
+        int a_range, b_range, k_left, steps_left;
+        // of the step being copied: offsets, out of range past its data, and ranges, empty past the last step.  (The
+        // range is checked against the lane's offset alone, so the whole of it goes there.)
+        unsigned oa, ob[2], os[NS];
+        int ra, rb;
     };
-    __device__ __forceinline__ static void dma_setup(Dma& d, const Fp8Args& a, int64_t m0, int64_t n0, int k_lo, int wave, int lane) {
-        const int w = wave & 3;
+    __device__ __forceinline__ static void dma_setup(Dma& d, const Fp8Args& a, int64_t m0, int64_t n0, int k_lo, int k_hi, int wave,
+                                                     int lane) {
         {
-            const int r = 8 * w + (lane >> 3), c = (lane & 7) ^ swz_a(r);
+            const int r = 8 * wave + (lane >> 3), c = (lane & 7) ^ swz_a(r);
             d.a_off = (unsigned)(r * (int)a.lda + 16 * c);
             d.a_k = 16 * c;
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // (the swizzle of rows 32 apart differs: two offsets)
-            const int r = 8 * (4 * q + w) + (lane >> 3), c = (lane & 7) ^ swz_b(r);
+        for (int q = 0; q < 2; ++q) {  // (with four waves the swizzle of rows 32 apart differs: two offsets)
+            const int r = 8 * (NW * q + wave) + (lane >> 3), c = (lane & 7) ^ swz_b(r);
             d.b_off[q] = (unsigned)(r * (int)a.ldb + 16 * c);
             d.b_k[q] = 16 * c;
         }
-        const int i = 64 * w + lane;
-        d.sa_off = i < BM && m0 + i < a.M ? (unsigned)(4 * i) : kOOB;
-        d.sb_off = i >= BN || n0 + i >= a.N ? kOOB : (BROW ? (unsigned)(4 * i) : (unsigned)(((i + (int)(n0 & 127)) >> 7) * (int)a.ldsb * 4));
+        const int i = 64 * (wave & 3) + lane;
+        const unsigned sa_off = i < BM && m0 + i < a.M ? (unsigned)(4 * i) : kOOB;
+        const unsigned sb_off =
+            i >= BN || n0 + i >= a.N ? kOOB : (BROW ? (unsigned)(4 * i) : (unsigned)(((i + (int)(n0 & 127)) >> 7) * (int)a.ldsb * 4));
+        const float* psa = a.sa + k_lo * a.ldsa + m0;
+        const float* psb = BROW ? a.sb + k_lo * a.ldsb + n0 : a.sb + n0 / 128 * a.ldsb + k_lo;
+#pragma unroll
+        for (int q = 0; q < NS; ++q) {
+            const bool of_b = NS == 2 ? q == 1 : wave >= 4;
+            d.s_off[q] = of_b ? sb_off : sa_off;
+            d.ps[q] = of_b ? psb : psa;
+            d.s_step[q] = of_b ? (BROW ? a.ldsb : 1) : a.ldsa;
+            d.s_lds[q] = (of_b ? SB_OFF : SA_OFF) + (wave & 3) * 256;
+        }
         const int64_t k0 = (int64_t)k_lo * 128;
         d.pa = a.A + m0 * a.lda + k0;
         d.pb = a.B + n0 * a.ldb + k0;
-        d.psa = a.sa + k_lo * a.ldsa + m0;
-        d.psb = BROW ? a.sb + k_lo * a.ldsb + n0 : a.sb + n0 / 128 * a.ldsb + k_lo;
-        d.sa_step = a.ldsa;
-        d.sb_step = BROW ? a.ldsb : 1;
-        d.a_hop = (unsigned)(32 * (int)a.lda);
-        d.b_hop = (unsigned)(64 * (int)a.ldb);
+        d.a_hop = (unsigned)(8 * NW * (int)a.lda);
+        d.b_hop = (unsigned)(16 * NW * (int)a.ldb);
         // the ranges end with the last row's last 16-byte chunk (which may hold bytes past K)
         const int left = (int)(a.K - k0);
         const int rows_a = min((int)a.M - (int)m0, BM), rows_b = min((int)a.N - (int)n0, BN);
         d.a_range = (rows_a - 1) * (int)a.lda + ((left + 15) & ~15);
         d.b_range = (rows_b - 1) * (int)a.ldb + ((left + 15) & ~15);
         d.k_left = left;
+        d.steps_left = k_hi - k_lo;
     }
     __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc(const void* p, int n) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, n, kRsrcWord3);
     }
-    // the copies of the next K-step into stage st
-    __device__ __forceinline__ static void dma_issue(Dma& d, lds_char* smem, int st, int wave) {
-        const int w = wave & 3;
-        lds_char* s = smem + st * STAGE;
-        if (NW == 4 || wave < 4) {
-            const __amdgpu_buffer_rsrc_t ra = rsrc(d.pa, d.a_range), rb = rsrc(d.pb, d.b_range);
-            const unsigned oa = d.a_k < d.k_left ? d.a_off : kOOB;
-            const unsigned ob[2] = {d.b_k[0] < d.k_left ? d.b_off[0] : kOOB, d.b_k[1] < d.k_left ? d.b_off[1] : kOOB};
+    // Copy `op` of the next step into the stage at s, ops in rising order.  Past the last step the copies run on with
+    // every lane out of range (zeros into a stage that is not read again): no branch splits the loop.
+    __device__ __forceinline__ static void dma_op(Dma& d, lds_char* s, int op, int wave) {
+        if (op == 0) {
+            const int left = d.steps_left > 0 ? d.k_left : 0;
+            d.ra = left > 0 ? d.a_range : 0;
+            d.rb = left > 0 ? d.b_range : 0;
+            d.oa = d.a_k < left ? d.a_off : kOOB;
+            d.ob[0] = d.b_k[0] < left ? d.b_off[0] : kOOB;
+            d.ob[1] = d.b_k[1] < left ? d.b_off[1] : kOOB;
 #pragma unroll
-            for (int j = 0; j < IA; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(s + (4 * j + w) * 1024), 16, oa, j * d.a_hop, 0, 0);
+            for (int q = 0; q < NS; ++q) d.os[q] = left > 0 ? d.s_off[q] : kOOB;
+        }
+        if (op < IA) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.pa, d.ra), (lds_void*)(s + (NW * op + wave) * 1024), 16, d.oa + op * d.a_hop, 0, 0,
+                                                     0);
+        } else if (op < IA + IB) {
+            const int j = op - IA;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.pb, d.rb), (lds_void*)(s + A_BYTES + (NW * j + wave) * 1024), 16,
+                                                     d.ob[j & 1] + (j >> 1) * d.b_hop, 0, 0, 0);
+        } else {
+            const int q = op - IA - IB;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.ps[q], (int)kOOB), (lds_void*)(s + d.s_lds[q]), 4, d.os[q], 0, 0, 0);
+        }
+        if (op == OPS - 1) {
+            d.pa += 128;
+            d.pb += 128;
 #pragma unroll
-            for (int j = 0; j < IB; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(s + A_BYTES + (4 * j + w) * 1024), 16, ob[j & 1],
-                                                         (j >> 1) * d.b_hop, 0, 0);
+            for (int q = 0; q < NS; ++q) d.ps[q] += d.s_step[q];
+            d.a_range -= 128;
+            d.b_range -= 128;
+            d.k_left -= 128;
+            --d.steps_left;
         }
-        if (NW == 4 || wave >= 4) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.psa, BM * 4), (lds_void*)(s + SA_OFF + w * 256), 4, d.sa_off, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.psb, (int)kOOB), (lds_void*)(s + SB_OFF + w * 256), 4, d.sb_off, 0, 0, 0);
-        }
-        d.pa += 128;
-        d.pb += 128;
-        d.psa += d.sa_step;
-        d.psb += d.sb_step;
-        d.a_range -= 128;
-        d.b_range -= 128;
-        d.k_left -= 128;
     }
-    // until at most `steps` K-steps of this wave's copies are in flight, and every LDS read has returned
-    __device__ __forceinline__ static void wait_copies(int steps, int wave) {
-        constexpr int OP = IA + IB;
-        if constexpr (NST > 2) {
-            if (steps >= 1) {
-                if (NW == 4) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(OP + 2) : "memory");
-                else if (wave < 4) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(OP) : "memory");
-                else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)" ::: "memory");
-                return;
-            }
-        }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // (__syncthreads would wait for the copies in flight)
+    __device__ __forceinline__ static void barrier() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     }
-    static_assert(NST <= 3, "wait_copies");
+    // until STEPS K-steps of this wave's copies are in flight, and every LDS read has returned
+    template <int STEPS>
+    __device__ __forceinline__ static void wait_copies() {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(STEPS * OPS) : "memory");
+    }
 
     // The last step of a K that is no multiple of 16: zeros for the bytes past K of the chunk that K ends in.
     __device__ __forceinline__ static void mask_tail(lds_char* smem, int st, int krem, int tid) {
@@ -310,12 +329,102 @@ struct Tile {
     // (keeps the compiler from sinking multiply-adds past the branches of the pipeline)
     __device__ __forceinline__ static void pin(f4& v) { asm volatile("" : "+v"(v)); }
 
+    // The copies of step kt + NST go out a few at a time, from the last group of step kt (whose stage is then free) into
+    // the groups of step kt + 1: sent in one piece they fill the address queue and hold the matrix cores up (8192^3
+    // 490 us, spread 465).  With two stages and two groups they have to land within the step: all at once.
+    static constexpr int SLOTS = NG >= 4 ? 12 : (NST > 2 ? 8 : 4);
+    static constexpr int PER_SLOT = (OPS + SLOTS - 1) / SLOTS;
+    __device__ __forceinline__ static void dma_slot(Dma& d, lds_char* s, int slot, int wave) {
+#pragma unroll
+        for (int i = 0; i < PER_SLOT; ++i)
+            if (slot < SLOTS && slot * PER_SLOT + i < OPS) dma_op(d, s, slot * PER_SLOT + i, wave);
+    }
+    static constexpr int slot_ops(int slot) {
+        return slot >= SLOTS || slot * PER_SLOT >= OPS ? 0 : (OPS - slot * PER_SLOT < PER_SLOT ? OPS - slot * PER_SLOT : PER_SLOT);
+    }
+
+    struct Pipe {
+        Rows fr[2];
+        Cols fc;
+        int st;
+    };
+    // One K-step from stage f.st.  MASK: the next one is the matrix's last and K no multiple of 16.
+    template <bool MASK>
+    __device__ __forceinline__ static void kstep(f4 (&acc)[FM][4], Pipe& f, Dma& d, const Lane& l, lds_char* smem, int k_tail,
+                                                 int wave) {
+        lds_char* s = smem + f.st * STAGE;
+        const int sn = f.st + 1 == NST ? 0 : f.st + 1;
+        const lds_char* nx = smem + sn * STAGE;
+        lds_char* before = smem + (f.st == 0 ? NST - 1 : f.st - 1) * STAGE;  // the stage of the step before
+        f4 p[2][GM];
+        float t[2][GM];
+        Operand<WIDE> ob[4];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            Rows& cur = f.fr[g & 1];
+            Rows& nxt = f.fr[(g + 1) & 1];
+            const bool end = g == NG - 1;
+#pragma unroll
+            for (int i = 0; i < GM; ++i) t[g & 1][i] = BROW ? cur.s[i] : cur.s[i] * f.fc.s[0][0];
+            Operand<WIDE> oa[GM];
+#pragma unroll
+            for (int i = 0; i < GM; ++i) oa[i] = operand<A5, WIDE>(cur.a[i]);
+            if (!end) {
+                read_rows(nxt, s, l, g + 1);
+            } else {
+                // every fragment of this step is in registers: the next step's copies must have landed, and those of
+                // step kt + NST may overwrite this stage
+#pragma unroll
+                for (int i = 0; i < FM - GM; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) pin(acc[i][j]);
+                wait_copies<NST - 2>();
+                barrier();
+                if constexpr (MASK) mask_tail(smem, sn, k_tail, threadIdx.x);
+                read_rows(nxt, nx, l, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int q = g * 4 + j, slot = end ? j : 4 + q;
+                if (g == 0) ob[j] = operand<B5, WIDE>(f.fc.b[j]);
+#pragma unroll
+                for (int i = 0; i < GM; ++i) p[q & 1][i] = mma<A5, B5, WIDE>(ob[j], oa[i]);
+                if (end) read_col(f.fc, nx, l, j);
+                dma_slot(d, end ? s : before, slot, wave);
+                if (q > 0) {  // the products before these
+                    const int g1 = (q - 1) >> 2, j1 = (q - 1) & 3;
+#pragma unroll
+                    for (int i = 0; i < GM; ++i) scale_add(acc[g1 * GM + i][j1], p[(q - 1) & 1][i], t[g1 & 1][i], f.fc, j1);
+                }
+                // in turn one product and the multiply-adds of the one GM before it
+#pragma unroll
+                for (int i = 0; i < GM; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
+                    if (end) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    else if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+                    if (i == 0 && slot_ops(slot) == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                    if (i == 0 && slot_ops(slot) == 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+                    if (i == 0 && slot_ops(slot) >= 3) __builtin_amdgcn_sched_group_barrier(0x020, 3, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < GM; ++i) scale_add(acc[FM - GM + i][3], p[1][i], t[(NG - 1) & 1][i], f.fc, 3);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pin(acc[i][j]);
+        read_scales(f.fc, nx, l);
+        f.st = sn;
+    }
+
     // K-steps [k_lo, k_hi) of tile (m0, n0)
     __device__ __forceinline__ static void mainloop(f4 (&acc)[FM][4], const Fp8Args& a, lds_char* smem, int64_t m0, int64_t n0,
                                                     int k_lo, int k_hi, int wave, int lane) {
         const int wm = wave / WN, wn = wave % WN;
         Dma d;
-        dma_setup(d, a, m0, n0, k_lo, wave, lane);
+        dma_setup(d, a, m0, n0, k_lo, k_hi, wave, lane);
         Lane l;
         {
             const int i = lane & 15, g = lane >> 4;
@@ -328,86 +437,30 @@ struct Tile {
             l.sa = SA_OFF + ra * 4;
             l.sb = SB_OFF + (wn * 64 + (BROW ? 16 * g : 0)) * 4;
         }
-        const int k_tail = (a.K & 15) ? (int)(a.K & 127) : 0;  // the step that needs mask_tail is the matrix's last
-        const int last = (int)((a.K + 127) / 128) - 1;
-        const int first = min(NST, k_hi - k_lo);
+        // the step that needs mask_tail is the matrix's last
+        const int last = (int)((a.K + 127) / 128) - 1, k_tail = (a.K & 15) && last < k_hi ? (int)(a.K & 127) : 0;
+        // the first NST steps' copies: all of step 0 .. NST - 2, and of step NST - 1 what a K-step before it would have sent
 #pragma unroll
         for (int i = 0; i < NST; ++i)
-            if (i < first) dma_issue(d, smem, i, wave);
-        wait_copies(0, wave);
-        __syncthreads();
+#pragma unroll
+            for (int op = 0; op < (i < NST - 1 ? OPS : min(4 * PER_SLOT, OPS)); ++op) dma_op(d, smem + i * STAGE, op, wave);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * OPS + (4 * PER_SLOT < OPS ? 4 * PER_SLOT : OPS)) : "memory");
+        barrier();
         if (k_tail && k_lo == last) mask_tail(smem, 0, k_tail, threadIdx.x);
-        Rows fr[2];
-        Cols fc;
-        Operand<WIDE> ob[4];
-        read_rows(fr[0], smem, l, 0);
+        Pipe f;
+        f.st = 0;
+        read_rows(f.fr[0], smem, l, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) read_col(fc, smem, l, j);
-        read_scales(fc, smem, l);
-        int st = 0;
-        for (int kt = k_lo; kt < k_hi; ++kt) {
-            const lds_char* s = smem + st * STAGE;
-            const int sn = st + 1 == NST ? 0 : st + 1;
-            const lds_char* nx = smem + sn * STAGE;
-            f4 p[2][GM];
-            float t[2][GM];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                Rows& cur = fr[g & 1];
-                Rows& nxt = fr[(g + 1) & 1];
-                const bool end = g == NG - 1;
-#pragma unroll
-                for (int i = 0; i < GM; ++i) t[g & 1][i] = BROW ? cur.s[i] : cur.s[i] * fc.s[0][0];
-                Operand<WIDE> oa[GM];
-#pragma unroll
-                for (int i = 0; i < GM; ++i) oa[i] = operand<A5, WIDE>(cur.a[i]);
-                if (!end) {
-                    read_rows(nxt, s, l, g + 1);
-                } else {
-                    // every fragment of this step is in registers: the next step's copies must have landed, and those
-                    // of step kt + NST may overwrite this stage
-#pragma unroll
-                    for (int i = 0; i < FM - GM; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) pin(acc[i][j]);
-                    wait_copies(kt + NST <= k_hi ? NST - 2 : 0, wave);
-                    __syncthreads();
-                    if (kt + NST < k_hi) dma_issue(d, smem, st, wave);
-                    if (k_tail && kt + 1 == last && kt + 1 < k_hi) mask_tail(smem, sn, k_tail, threadIdx.x);
-                    read_rows(nxt, nx, l, 0);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int q = g * 4 + j;
-                    if (g == 0) ob[j] = operand<B5, WIDE>(fc.b[j]);
-#pragma unroll
-                    for (int i = 0; i < GM; ++i) p[q & 1][i] = mma<A5, B5, WIDE>(ob[j], oa[i]);
-                    if (end) read_col(fc, nx, l, j);
-                    if (q > 0) {  // the products before these
-                        const int g1 = (q - 1) >> 2, j1 = (q - 1) & 3;
-#pragma unroll
-                        for (int i = 0; i < GM; ++i) scale_add(acc[g1 * GM + i][j1], p[(q - 1) & 1][i], t[g1 & 1][i], fc, j1);
-                    }
-                    // in turn one product and the multiply-adds of the one GM before it
-#pragma unroll
-                    for (int i = 0; i < GM; ++i) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
-                        if (end) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                        else if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < GM; ++i) scale_add(acc[FM - GM + i][3], p[1][i], t[(NG - 1) & 1][i], fc, 3);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) pin(acc[i][j]);
-            read_scales(fc, nx, l);
-            st = sn;
+        for (int j = 0; j < 4; ++j) read_col(f.fc, smem, l, j);
+        read_scales(f.fc, smem, l);
+        int kt = k_lo;
+        const int plain = k_tail && k_lo < last ? last - 1 : k_hi;
+        for (; kt < plain; ++kt) kstep<false>(acc, f, d, l, smem, 0, wave);
+        if (kt < k_hi) {
+            kstep<true>(acc, f, d, l, smem, k_tail, wave);
+            kstep<false>(acc, f, d, l, smem, 0, wave);
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // (nothing lands in LDS after the workgroup)
     }
 
     __device__ __forceinline__ static void run(const Fp8Args& a) {
