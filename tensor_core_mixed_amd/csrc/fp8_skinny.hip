@@ -161,8 +161,16 @@ __global__ __launch_bounds__(kThreads) void fp8_skinny_kernel(Fp8Args a) {
 __global__ __launch_bounds__(256) void fp8_skinny_sum_kernel(Fp8Args a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, mn = a.M * a.N;
     if (i >= mn) return;
-    float v = a.ws[i];
-    for (int s = 1; s < a.split; ++s) v += a.ws[s * mn + i];
+    float v = 0.f;
+    for (int s = 0; s < a.split; s += 8) {
+        float x[8];  // (in flight together)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (s + u < a.split) x[u] = a.ws[(s + u) * mn + i];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (s + u < a.split) v += x[u];
+    }
     store_epilogue(a, v, i / a.N, i % a.N);
 }
 

@@ -86,35 +86,35 @@ __device__ __forceinline__ f4 mma(const Operand<WIDE>& b, const Operand<WIDE>& a
     }
 }
 
-// 16 consecutive columns n .. n+15 of row m: accumulators to C
 struct Epilogue {
-    // v[16] += bias and C's contents, ReLU, store; full: all 16 columns exist
-    __device__ __forceinline__ static void row16(const Fp8Args& a, float (&v)[16], int64_t m, int64_t n) {
-        const bool full = n + 16 <= a.N;
+    // E consecutive columns n .. of row m: v += bias and C's contents, ReLU, stored in C's type
+    template <int E>
+    __device__ __forceinline__ static void row(const Fp8Args& a, float (&v)[E], int64_t m, int64_t n) {
+        const bool full = n + E <= a.N;
         if (a.has_bias) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < E; ++j)
                 if (full || n + j < a.N) v[j] += load_float<F32>((const char*)a.bias, n + j);
         }
         char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
         const int cs = c_elem_bytes(a.c_type);
         if (a.accum) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < E; ++j)
                 if (full || n + j < a.N) v[j] += load_c_any(c + j * cs, a.c_type);
         }
         if (a.relu) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = v[j] > 0.f ? v[j] : 0.f;
+            for (int j = 0; j < E; ++j) v[j] = v[j] > 0.f ? v[j] : 0.f;
         }
         if (full && a.c_vec) {
             if (a.c_type == C_ACC) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) *(f4*)(c + 16 * q) = f4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                for (int q = 0; q < E / 4; ++q) *(f4*)(c + 16 * q) = f4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
             } else {
-                i4 w[2];
+                unsigned w[E / 2];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < E / 2; ++q) {
                     unsigned lo, hi;
                     if (a.c_type == C_F16) {
                         lo = __builtin_bit_cast(unsigned short, (_Float16)v[2 * q]);
@@ -123,14 +123,13 @@ struct Epilogue {
                         lo = __builtin_bit_cast(unsigned short, (__bf16)v[2 * q]);
                         hi = __builtin_bit_cast(unsigned short, (__bf16)v[2 * q + 1]);
                     }
-                    w[q >> 2][q & 3] = (int)(lo | hi << 16);
+                    w[q] = lo | hi << 16;
                 }
-                *(i4*)c = w[0];
-                *(i4*)(c + 16) = w[1];
+                __builtin_memcpy(__builtin_assume_aligned(c, E >= 8 ? 16 : 8), w, 2 * E);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < E; ++j)
                 if (n + j < a.N) store_c_any(c + j * cs, a.c_type, v[j]);
         }
     }
@@ -499,14 +498,15 @@ struct Tile {
             float v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = acc[i][e >> 2][e & 3];
-            Epilogue::row16(a, v, m, n);
+            Epilogue::row<16>(a, v, m, n);
         }
     }
 
-    // Sum of a split launch: one wave takes the 16 rows x 64 columns of one (tile, wave, row tile), adds the shares'
-    // partials in order and stores them.
+    // Sum of a split launch: a wave takes one accumulator tile (16 rows by four columns a lane) and has up to eight
+    // shares' partials of it in flight (one after the other, eleven shares of 37 rows took 6.3 us); they are added in
+    // order.
     __device__ __forceinline__ static void run_sum(const Fp8Args& a) {
-        const int lane = threadIdx.x & 63;
+        const int lane = threadIdx.x & 63, j = threadIdx.x >> 6;
         const int64_t T = (int64_t)a.tiles_m * a.tiles_n;
         int64_t b = blockIdx.x;
         const int i = (int)(b % FM);
@@ -516,22 +516,22 @@ struct Tile {
         int tm, tn;
         super_order(t, a.tiles_m, a.tiles_n, a.group_m, a.super_m, a.super_n, &tm, &tn);
         const int wm = wave / WN, wn = wave % WN;
-        const int64_t m = (int64_t)tm * BM + wm * TM + 16 * i + (lane & 15), n = (int64_t)tn * BN + wn * 64 + 16 * (lane >> 4);
+        const int64_t m = (int64_t)tm * BM + wm * TM + 16 * i + (lane & 15), n = (int64_t)tn * BN + wn * 64 + 16 * (lane >> 4) + 4 * j;
         if (m >= a.M || n >= a.N) return;
-        const f4* p = (const f4*)a.ws + (((int64_t)t * NW + wave) * FM + i) * 4 * 64 + lane;
+        const f4* p = (const f4*)a.ws + ((((int64_t)t * NW + wave) * FM + i) * 4 + j) * 64 + lane;
         const int64_t step = T * NW * FM * 4 * 64;
-        f4 s[4];
+        f4 s = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < a.split; k += 8) {
+            f4 x[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = p[j * 64];
-        for (int k = 1; k < a.split; ++k) {
-            p += step;
+            for (int u = 0; u < 8; ++u)
+                if (k + u < a.split) x[u] = p[(k + u) * step];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] += p[j * 64];
+            for (int u = 0; u < 8; ++u)
+                if (k + u < a.split) s += x[u];
         }
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = s[e >> 2][e & 3];
-        Epilogue::row16(a, v, m, n);
+        float v[4] = {s[0], s[1], s[2], s[3]};
+        Epilogue::row<4>(a, v, m, n);
     }
 };
 

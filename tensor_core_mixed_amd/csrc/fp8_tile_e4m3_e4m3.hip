@@ -8,13 +8,13 @@ int launch_fp8_tile_e4m3_e4m3(int cfg, const Fp8Args& a, void* stream) {
 // the sum of a split launch's partial tiles (the operands' types play no part)
 namespace fp8t {
 template <int CFG>
-__global__ __launch_bounds__(64) void fp8_tile_sum_kernel(Fp8Args a) {
+__global__ __launch_bounds__(256) void fp8_tile_sum_kernel(Fp8Args a) {
     Tile<CFG, false, false, false, false>::run_sum(a);
 }
 template <int CFG>
 int launch_sum(const Fp8Args& a, hipStream_t s) {
     using T = Tile<CFG, false, false, false, false>;
-    hipLaunchKernelGGL((fp8_tile_sum_kernel<CFG>), dim3((unsigned)(a.tiles_m * a.tiles_n * T::NW * T::FM)), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((fp8_tile_sum_kernel<CFG>), dim3((unsigned)(a.tiles_m * a.tiles_n * T::NW * T::FM)), dim3(256), 0, s, a);
     return (int)hipGetLastError();
 }
 }  // namespace fp8t

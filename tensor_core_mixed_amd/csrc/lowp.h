@@ -59,7 +59,7 @@ constexpr Fp8Tile kFp8Tiles[kNumFp8Tiles] = {
     {256, 256, 2, 4, 2, false},  // large products: 128 x 64 a wave, two waves a SIMD
     {256, 128, 4, 2, 3, true},  // half as many columns, three stages
     {128, 128, 2, 2, 2, true},  // two workgroups a CU
-    {64, 128, 2, 2, 2, true},   // few rows
+    {64, 128, 2, 2, 3, true},   // few rows
 };
 // A, B and sizes as fp8_tiles_fit accepts; the operand types pick the instance
 int launch_fp8_tile_e4m3_e4m3(int cfg, const Fp8Args& a, void* stream);
