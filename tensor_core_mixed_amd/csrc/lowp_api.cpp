@@ -99,10 +99,11 @@ bool fp8_tiles_fit(const Fp8Args& a) {
            !(a.ldb & 15) && a.lda < lim && a.ldb < lim && a.ldsb < ((int64_t)1 << 26);
 }
 // The macro tile and the k ranges of a product by a model of its time, in
-// microseconds: a workgroup's K-steps, one at a time on a CU or `per_cu` of
-// them sharing it, and for a split the sum's launch and the partial tiles'
-// way through the caches.  Step times fitted to products of 64 to 8192 rows,
-// 8-bit and (binary32 C) 16-bit operands.
+// microseconds: a workgroup's K-steps, whose time grows from `lone` to
+// `shared` as the chip fills; the operands' way from memory at least; and for
+// a split the sum's launch and the partial tiles' way through the caches.
+// Fitted to products of 37 to 8192 rows, 8-bit and (binary32 C) 16-bit
+// operands.
 struct Fp8Plan {
     int config, split;
 };
@@ -110,12 +111,13 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
     static constexpr struct {
         int per_cu;
         double lone, shared, lone_wide, shared_wide;
-    } kStep[kNumFp8Tiles] = {{1, 2.0, 2.0, 0, 0}, {1, 1.1, 1.25, 2.3, 2.7}, {2, 0.75, 1.15, 1.3, 2.3}, {2, 0.6, 0.78, 0.8, 1.35}};
-    constexpr double kFixed = 3.0, kSum = 4.0, kBytesPerUs = 5e6;
+    } kStep[kNumFp8Tiles] = {{1, 1.45, 1.9, 0, 0}, {1, 0.78, 1.04, 1.7, 2.15}, {2, 0.78, 1.17, 1.2, 2.3}, {2, 0.47, 0.73, 0.81, 1.28}};
+    constexpr double kFixed = 3.0, kSum = 2.5, kShare = 0.08, kBytesPerUs = 5e6;
     Fp8Plan best{kFp8Generic, 1};
     if (!fp8_tiles_fit(a) || o.fp8_config == kFp8Generic) return best;
     const bool wide = a.c_type == C_ACC;
     const int64_t steps = scale_blocks(a.K);
+    const double memory = (double)(a.M + a.N) * (double)a.K / kBytesPerUs;
     double best_t = 1e30;
     int forced = o.fp8_config;
     if (forced >= 0 && forced < kNumFp8Tiles && wide && !kFp8Tiles[forced].wide) forced = -1;  // cannot serve
@@ -129,9 +131,9 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
             if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
             const int64_t wgs = tiles * s, rest = wgs % slots;
-            const double step = (double)(wgs / slots) * shared + (rest == 0 ? 0 : (rest <= 256 ? lone : shared));
-            const double time = kFixed + (double)((steps + s - 1) / s) * step +
-                                (s > 1 ? kSum + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            const double step = (double)(wgs / slots) * shared + (rest == 0 ? 0 : lone + (shared - lone) * (double)rest / (double)slots);
+            const double time = kFixed + std::max((double)((steps + s - 1) / s) * step, memory) +
+                                (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t) best_t = time, best = {c, s};
         }
     }
@@ -143,8 +145,8 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         const double round = kRound[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
         for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
             if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
-            const double time = kFixed + (double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round +
-                                (s > 1 ? kSum + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            const double time = kFixed + std::max((double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round, memory) +
+                                (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t) best_t = time, best = {kFp8Skinny, s};
         }
     }
