@@ -7,12 +7,14 @@
 //
 // The chosen experts' weights bind the time, and each is read once: a
 // workgroup takes one expert and a block of its rows (16 of gate and up, 64
-// of W2) and multiplies them with all pairs of that expert, 32 at
-// a time, on 16x16x32 MFMAs with the weights' rows as one operand and the
-// pairs as the other.  Weights go straight from memory to registers; eight
+// of W2) and multiplies them with all pairs of that expert, 16 or 32
+// at a time, on 16x16x32 MFMAs with the weights' rows as one operand and the
+// pairs as the other.  Weights go straight from memory to registers; the
 // waves deal k among themselves, the loads of the next steps in flight, and
 // add their sums in LDS in wave order.  Every workgroup finds its pairs itself
-// by one pass over the ids.  Three launches: up, down, sum over the slots.
+// by one pass over the ids.  Three launches: up, down, sum over the slots.  (The
+// sum left to the last workgroup of 64 columns took one token of eight experts
+// from 17.9 to 17.3 us and four tokens from 47.5 to 48.6.)
 //
 // 8-bit weights are taken to 16-bit floats (exactly) and a 128-wide block's
 // sums scaled by its tile's scale.  h is binary32 in memory and goes to the
@@ -32,8 +34,10 @@ typedef int i4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kUpRows = 16, kDownTiles = 4, kDownRows = 16 * kDownTiles;
+// Four waves a workgroup: with eight, a kernel past 128 registers leaves a CU one workgroup (24 bf16 tokens 243 us, 222
+// with four and 237 with two; one token of eight experts 4096 x 1536 in 8 bits 46, 43 and 48).
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kUpRows = 16;
 
 // eight operand values of a lane, as raw bits of either 16-bit type
 template <int XT>
@@ -63,10 +67,12 @@ __device__ __forceinline__ i4 load16(const char* p) {
     return v;
 }
 __device__ __forceinline__ i4 load16_part(const char* p, int64_t left) {
-    i4 v = {0, 0, 0, 0};
+    i4 v;
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-        if (4 * d < left) v[d] = ((const int*)p)[d];  // (rows are whole words)
+    for (int d = 0; d < 4; ++d) {  // (rows are whole words; words past the row read its last)
+        const int x = *(const int*)(p + min<int64_t>(4 * d, left - 4));
+        v[d] = 4 * d < left ? x : 0;
+    }
     return v;
 }
 
@@ -76,6 +82,17 @@ __device__ __forceinline__ i4 load16_part(const char* p, int64_t left) {
 __device__ __forceinline__ int find_pairs(const MoeArgs& a, int slot, int* list, int* counts, int& e) {
     const int P = a.tokens * a.topk, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const bool by_pair = P < a.experts;
+    if (P <= 64) {
+        // every wave by itself, from one load: all write the same list, and each reads what it wrote
+        const int id = lane < P ? a.ids[lane] : -1;
+        e = by_pair ? __builtin_amdgcn_readlane(id, slot) : slot;
+        if ((unsigned)e >= (unsigned)a.experts) return 0;
+        const unsigned long long m = __ballot(id == e);
+        if (m == 0 || (by_pair && __builtin_ctzll(m) != slot)) return 0;
+        if (id == e) list[__builtin_popcountll(m & ((1ull << lane) - 1))] = lane;
+        __builtin_amdgcn_wave_barrier();
+        return __builtin_popcountll(m);
+    }
     e = by_pair ? a.ids[slot] : slot;
     if ((unsigned)e >= (unsigned)a.experts) return 0;
     int total = 0;
@@ -114,10 +131,12 @@ struct Up {
         const char *w[2], *x[MT];
         const float* s[2];
     };
+    // step kt, whole or (PART) the row's last
+    template <bool PART>
     __device__ __forceinline__ static void load(Step& t, const Src& s, const MoeArgs& a, int kt, int lane) {
         const int k = kt * 64 + 16 * (lane >> 4);
         constexpr int ES = W8 ? 1 : 2;
-        if (kt * 64 + 64 <= a.hidden) {
+        if constexpr (!PART) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -186,21 +205,29 @@ struct Up {
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[m][i] = f4{0.f, 0.f, 0.f, 0.f};
-        const int steps = (a.hidden + 63) / 64;
+        constexpr int OUT = (MT * 256 + kThreads - 1) / kThreads;  // results a thread
+        float weight[OUT];
+#pragma unroll
+        for (int o = 0; o < OUT; ++o) weight[o] = a.weights[list[min((tid + o * kThreads) >> 4, n - 1)]];
+        const int steps = a.hidden / 64;  // whole ones
         Step t[kAhead + 1];
         int kt = wave;
 #pragma unroll
         for (int u = 0; u <= kAhead; ++u)
-            if (kt + u * kWaves < steps) load(t[u], s, a, kt + u * kWaves, lane);
+            if (kt + u * kWaves < steps) load<false>(t[u], s, a, kt + u * kWaves, lane);
         while (kt < steps) {
 #pragma unroll
             for (int u = 0; u <= kAhead; ++u) {
                 if (kt < steps) {
                     multiply(acc, t[u]);
-                    if (kt + (kAhead + 1) * kWaves < steps) load(t[u], s, a, kt + (kAhead + 1) * kWaves, lane);
+                    if (kt + (kAhead + 1) * kWaves < steps) load<false>(t[u], s, a, kt + (kAhead + 1) * kWaves, lane);
                 }
                 kt += kWaves;
             }
+        }
+        if (a.hidden % 64 != 0 && wave == steps % kWaves) {
+            load<true>(t[0], s, a, steps, lane);
+            multiply(acc, t[0]);
         }
         __syncthreads();  // (part may still be read by a pass before)
 #pragma unroll
@@ -208,39 +235,43 @@ struct Up {
 #pragma unroll
             for (int i = 0; i < MT; ++i) part[((wave * 2 + m) * MT + i) * 64 + lane] = acc[m][i];
         __syncthreads();
-        if (tid >= MT * 256) return;
-        const int c = tid >> 4, i = tid & 15;  // pair of the pass, row of the block
-        const float* q = (const float*)(part + (c >> 4) * 64 + (i >> 2) * 16 + (c & 15)) + (i & 3);
-        float g = 0.f, u = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            g += q[(w * 2) * MT * 256];
-            u += q[(w * 2 + 1) * MT * 256];
-        }
-        const bool live = c < n && i0 + i < a.inter;
-        const int p = list[min(c, n - 1)];
-        const float h = live ? a.weights[p] * (g / (1.f + expf(-g)) * u) : 0.f;
-        if (live) ((float*)a.ws)[(int64_t)p * a.inter + i0 + i] = h;
-        if constexpr (XT == F16 && !W8) {
-            unsigned m = __builtin_bit_cast(unsigned, h) & 0x7fffffffu;
-            for (int o = 8; o; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o));
-            if (i == 0 && c < n) a.hmax[(int64_t)p * ((a.inter + kUpRows - 1) / kUpRows) + i0 / kUpRows] = m;
+        for (int o = 0; o < OUT; ++o) {
+            const int x = tid + o * kThreads;
+            if (x >= MT * 256) return;
+            const int c = x >> 4, i = x & 15;  // pair of the pass, row of the block
+            const float* q = (const float*)(part + (c >> 4) * 64 + (i >> 2) * 16 + (c & 15)) + (i & 3);
+            float g = 0.f, u = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                g += q[(w * 2) * MT * 256];
+                u += q[(w * 2 + 1) * MT * 256];
+            }
+            const bool live = c < n && i0 + i < a.inter;
+            const int p = list[min(c, n - 1)];
+            const float h = live ? weight[o] * (g / (1.f + expf(-g)) * u) : 0.f;
+            if (live) ((float*)a.ws)[(int64_t)p * a.inter + i0 + i] = h;
+            if constexpr (XT == F16 && !W8) {
+                unsigned m = __builtin_bit_cast(unsigned, h) & 0x7fffffffu;
+                for (int d = 8; d; d >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, d));
+                if (i == 0 && c < n) a.hmax[(int64_t)p * ((a.inter + kUpRows - 1) / kUpRows) + i0 / kUpRows] = m;
+            }
         }
     }
 };
 
-template <int XT, bool W8>
+template <int XT, bool W8, int MT>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
-    __shared__ f4 part[kWaves * 2 * 2 * 64];
+    __shared__ f4 part[kWaves * 2 * MT * 64];
     __shared__ int list[kMoePairs], counts[kWaves];
     const int blocks = (a.inter + kUpRows - 1) / kUpRows;
     const int slot = blockIdx.x / blocks, i0 = (blockIdx.x % blocks) * kUpRows;
     int e;
     const int n = find_pairs(a, slot, list, counts, e);
-    for (int j = 0; j < n; j += 32) {
-        const int left = min(n - j, 32);
+    for (int j = 0; j < n; j += 16 * MT) {
+        const int left = min(n - j, 16 * MT);
         if (left <= 16) Up<XT, W8, 1>::run(a, e, i0, list + j, left, part);
-        else Up<XT, W8, 2>::run(a, e, i0, list + j, left, part);
+        else if constexpr (MT > 1) Up<XT, W8, MT>::run(a, e, i0, list + j, left, part);
     }
 }
 
@@ -268,7 +299,10 @@ __device__ __forceinline__ void split8(const f4 (&v)[2], float f, i4& hi, i4& lo
     }
 }
 
-// A step is 32 k of 64 rows (8-bit weights: 64 k): 16 bytes of a row a lane.
+// Row tiles of W2 a workgroup: h is split into its 16-bit parts once for four (with two, 8% slower).
+constexpr int kDownTiles = 4, kDownRows = 16 * kDownTiles;
+
+// A step is 32 k (8-bit weights: 64 k): 16 bytes of a row a lane.
 template <int HT, bool W8, int MT>
 struct Down {
     static constexpr int KV = W8 ? 2 : 1, KS = 32 * KV;
@@ -282,10 +316,12 @@ struct Down {
         const char* w[kDownTiles];
         const float *h[MT], *s;
     };
+    // step kt, whole or (PART) the row's last
+    template <bool PART>
     __device__ __forceinline__ static void load(Step& t, const Src& s, const MoeArgs& a, int kt, int lane) {
         const int k = kt * KS + 8 * KV * (lane >> 4);
         constexpr int ES = W8 ? 1 : 2;
-        if (kt * KS + KS <= a.inter) {
+        if constexpr (!PART) {
 #pragma unroll
             for (int j = 0; j < kDownTiles; ++j) t.w[j] = load16(s.w[j] + (int64_t)k * ES);
 #pragma unroll
@@ -366,21 +402,25 @@ struct Down {
         for (int j = 0; j < kDownTiles; ++j)
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[j][i] = f4{0.f, 0.f, 0.f, 0.f};
-        const int steps = (a.inter + KS - 1) / KS;
+        const int steps = a.inter / KS;  // whole ones
         Step t[kAhead + 1];
         int kt = wave;
 #pragma unroll
         for (int u = 0; u <= kAhead; ++u)
-            if (kt + u * kWaves < steps) load(t[u], s, a, kt + u * kWaves, lane);
+            if (kt + u * kWaves < steps) load<false>(t[u], s, a, kt + u * kWaves, lane);
         while (kt < steps) {
 #pragma unroll
             for (int u = 0; u <= kAhead; ++u) {
                 if (kt < steps) {
                     multiply(acc, t[u], f);
-                    if (kt + (kAhead + 1) * kWaves < steps) load(t[u], s, a, kt + (kAhead + 1) * kWaves, lane);
+                    if (kt + (kAhead + 1) * kWaves < steps) load<false>(t[u], s, a, kt + (kAhead + 1) * kWaves, lane);
                 }
                 kt += kWaves;
             }
+        }
+        if (a.inter % KS != 0 && wave == steps % kWaves) {
+            load<true>(t[0], s, a, steps, lane);
+            multiply(acc, t[0], f);
         }
         __syncthreads();  // (part may still be read by a pass before)
 #pragma unroll
@@ -401,19 +441,20 @@ struct Down {
     }
 };
 
-template <int HT, bool W8>
+template <int XT, bool W8, int MT>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
-    __shared__ f4 part[kWaves * kDownTiles * 2 * 64];
-    __shared__ float power[32];
+    constexpr int HT = W8 ? BF16 : XT;  // (8-bit weights are exact in either type)
+    __shared__ f4 part[kWaves * kDownTiles * MT * 64];
+    __shared__ float power[16 * MT];
     __shared__ int list[kMoePairs], counts[kWaves];
     const int blocks = (a.hidden + kDownRows - 1) / kDownRows;
     const int slot = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kDownRows;
     int e;
     const int n = find_pairs(a, slot, list, counts, e);
-    for (int j = 0; j < n; j += 32) {
-        const int left = min(n - j, 32);
+    for (int j = 0; j < n; j += 16 * MT) {
+        const int left = min(n - j, 16 * MT);
         if (left <= 16) Down<HT, W8, 1>::run(a, e, c0, list + j, left, part, power);
-        else Down<HT, W8, 2>::run(a, e, c0, list + j, left, part, power);
+        else if constexpr (MT > 1) Down<HT, W8, MT>::run(a, e, c0, list + j, left, part, power);
     }
 }
 
@@ -424,21 +465,35 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
     const int c = (int)(n - t * a.hidden);
     if (t >= a.tokens) return;
     float v = 0.f;
-    for (int j = 0; j < a.topk; ++j) {
-        const int64_t p = t * a.topk + j;
-        if ((unsigned)a.ids[p] < (unsigned)a.experts) v += a.y[p * a.hidden + c];
+    for (int j = 0; j < a.topk; j += 8) {
+        float y[8];  // (loads in flight together; a slot that adds nothing has no y)
+        int e[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t p = t * a.topk + min(j + u, a.topk - 1);
+            e[u] = a.ids[p];
+            y[u] = a.y[p * a.hidden + c];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (j + u < a.topk && (unsigned)e[u] < (unsigned)a.experts) v += y[u];
     }
     store_c_any((char*)a.out + (t * a.ldo + c) * 2, XT == F16 ? C_F16 : C_BF16, v);
 }
 
-template <int XT, bool W8>
-int launch(const MoeArgs& a, hipStream_t s) {
-    constexpr int HT = W8 ? BF16 : XT;  // (8-bit weights are exact in either type)
+template <int XT, bool W8, int MT>
+void launch_products(const MoeArgs& a, hipStream_t s) {
     const int slots = min(a.tokens * a.topk, a.experts);
     const dim3 up((unsigned)(slots * ((a.inter + kUpRows - 1) / kUpRows)));
     const dim3 down((unsigned)(slots * ((a.hidden + kDownRows - 1) / kDownRows)));
-    hipLaunchKernelGGL((moe_up_kernel<XT, W8>), up, dim3(kThreads), 0, s, a);
-    hipLaunchKernelGGL((moe_down_kernel<HT, W8>), down, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((moe_up_kernel<XT, W8, MT>), up, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<XT, W8, MT>), down, dim3(kThreads), 0, s, a);
+}
+template <int XT, bool W8>
+int launch(const MoeArgs& a, hipStream_t s) {
+    // an expert has a pair of every token at most (unless a token names it twice): 16 at a time, or up to 32
+    if (a.tokens <= 16) launch_products<XT, W8, 1>(a, s);
+    else launch_products<XT, W8, 2>(a, s);
     hipLaunchKernelGGL((moe_sum_kernel<XT>), dim3((unsigned)(((int64_t)a.tokens * a.hidden + 255) / 256)), dim3(256), 0, s, a);
     return (int)hipGetLastError();
 }
