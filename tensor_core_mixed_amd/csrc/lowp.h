@@ -3,7 +3,9 @@
 // tcm_quantize_fp8, tcm_moe_route, tcm_moe), shared by the C ABI and the
 // kernels.
 #pragma once
+#include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 namespace tcm {
 
@@ -120,5 +122,9 @@ LowpOpts lowp_opts();
 // workspace, grown to `bytes` (a tcm_status), and the text of tcm_last_plan.
 int workspace_for(void* stream, int64_t bytes, void** out);
 void set_last_plan(const char* text);
+// (formatted when it is asked for)
+constexpr int kPlanValues = 10;
+using PlanFormat = void (*)(char* buf, size_t n, const int64_t* v);
+void set_last_plan(PlanFormat format, std::initializer_list<int64_t> v);
 
 }  // namespace tcm

@@ -84,10 +84,12 @@ int quantize_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dt
     a.ldqt = ldqt;
     a.st = st;
     a.ldst = ldst;
-    char text[160];
-    snprintf(text, sizeof text, "kernel=quantize rows=%lld cols=%lld dtype=%d e5m2=%d block=%s out=%s", (long long)rows,
-             (long long)cols, t, (flags & TCM_Q_E5M2) != 0, tile ? "tile" : "row", q ? (qt ? "both" : "rows") : "cols");
-    set_last_plan(text);
+    set_last_plan(
+        [](char* buf, size_t n, const int64_t* v) {
+            snprintf(buf, n, "kernel=quantize rows=%lld cols=%lld dtype=%d e5m2=%d block=%s out=%s", (long long)v[0], (long long)v[1],
+                     (int)v[2], (int)v[3], v[4] ? "tile" : "row", v[5] ? (v[6] ? "both" : "rows") : "cols");
+        },
+        {rows, cols, t, (flags & TCM_Q_E5M2) != 0, tile, q != nullptr, qt != nullptr});
     return done(launch_quantize(t, flags & TCM_Q_E5M2, tile, a, stream));
 }
 
@@ -203,13 +205,15 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
     a.accum = (epilogue & TCM_EPI_ACCUM) != 0;
     a.c_type = c_type;
     a.c_vec = ((uintptr_t)C & 15) == 0 && ((ldc * c_elem_bytes(c_type)) & 15) == 0;
-    char text[160];
     const Fp8Plan pl = plan_fp8(a, lowp_opts());
     if (pl.config == kFp8Generic) {
         // (a launch counts its threads in 32 bits)
         if (((M + 63) / 64) * ((N + 63) / 64) >= ((int64_t)1 << 24)) return TCM_ERR_NOT_SUPPORTED;
-        snprintf(text, sizeof text, "kernel=fp8_generic M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
-        set_last_plan(text);
+        set_last_plan(
+            [](char* buf, size_t n, const int64_t* v) {
+                snprintf(buf, n, "kernel=fp8_generic M=%lld N=%lld K=%lld", (long long)v[0], (long long)v[1], (long long)v[2]);
+            },
+            {M, N, K});
         return done(launch_fp8_generic(a, stream));
     }
     const bool skinny = pl.config == kFp8Skinny;
@@ -229,9 +233,12 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
         if (st != TCM_OK) return st;
         a.ws = (float*)ws;
     }
-    snprintf(text, sizeof text, "kernel=fp8_%s tile=%dx%d tiles=%lld split=%d M=%lld N=%lld K=%lld", skinny ? "skinny" : "tile",
-             t.bm, t.bn, (long long)(tm * tn), a.split, (long long)M, (long long)N, (long long)K);
-    set_last_plan(text);
+    set_last_plan(
+        [](char* buf, size_t n, const int64_t* v) {
+            snprintf(buf, n, "kernel=fp8_%s tile=%dx%d tiles=%lld split=%d M=%lld N=%lld K=%lld", v[0] ? "skinny" : "tile", (int)v[1],
+                     (int)v[2], (long long)v[3], (int)v[4], (long long)v[5], (long long)v[6], (long long)v[7]);
+        },
+        {skinny, t.bm, t.bn, tm * tn, a.split, M, N, K});
     if (skinny) return done(launch_fp8_skinny(t.bm, a, stream));
     const auto launch = a.a_e5m2 ? (a.b_e5m2 ? launch_fp8_tile_e5m2_e5m2 : launch_fp8_tile_e5m2_e4m3)
                                  : (a.b_e5m2 ? launch_fp8_tile_e4m3_e5m2 : launch_fp8_tile_e4m3_e4m3);
@@ -269,10 +276,12 @@ int route_impl(int64_t tokens, int64_t experts, int64_t topk, const void* logits
     a.scale = scale;
     a.ids = ids;
     a.weights = weights;
-    char text[160];
-    snprintf(text, sizeof text, "kernel=route tokens=%lld experts=%lld topk=%lld dtype=%d%s%s%s", (long long)tokens,
-             (long long)experts, (long long)topk, t, a.sigmoid ? " sigmoid=1" : "", a.norm ? " norm=1" : "", bias ? " bias=1" : "");
-    set_last_plan(text);
+    set_last_plan(
+        [](char* buf, size_t n, const int64_t* v) {
+            snprintf(buf, n, "kernel=route tokens=%lld experts=%lld topk=%lld dtype=%d%s%s%s", (long long)v[0], (long long)v[1],
+                     (long long)v[2], (int)v[3], v[4] ? " sigmoid=1" : "", v[5] ? " norm=1" : "", v[6] ? " bias=1" : "");
+        },
+        {tokens, experts, topk, t, a.sigmoid, a.norm, bias != nullptr});
     return done(launch_route(t, a, stream));
 }
 
@@ -315,7 +324,6 @@ int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int
     a.inter = (int)inter;
     a.experts = (int)experts;
     a.topk = work ? (int)topk : 0;
-    char text[200];
     // whole words in every row: the tiled kernels, in calls of kMoePairs pairs at most
     const int64_t per_word = w8 ? 4 : 2;
     const auto words = [](const void* p) { return ((uintptr_t)p & 3) == 0; };
@@ -330,10 +338,13 @@ int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int
     if (st != TCM_OK) return st;
     a.y = (float*)((char*)a.ws + h_bytes);
     a.hmax = (unsigned*)((char*)a.ws + h_bytes + y_bytes);
-    snprintf(text, sizeof text, "kernel=moe_%s tokens=%lld hidden=%lld inter=%lld experts=%lld topk=%lld dtype=%d e4m3=%d",
-             tiled ? "tile" : "generic", (long long)tokens, (long long)hidden, (long long)inter, (long long)experts, (long long)topk, t,
-             (int)w8);
-    set_last_plan(text);
+    set_last_plan(
+        [](char* buf, size_t n, const int64_t* v) {
+            snprintf(buf, n, "kernel=moe_%s tokens=%lld hidden=%lld inter=%lld experts=%lld topk=%lld dtype=%d e4m3=%d",
+                     v[0] ? "tile" : "generic", (long long)v[1], (long long)v[2], (long long)v[3], (long long)v[4], (long long)v[5],
+                     (int)v[6], (int)v[7]);
+        },
+        {tiled, tokens, hidden, inter, experts, topk, t, w8});
     for (int64_t t0 = 0; t0 < tokens; t0 += chunk) {
         a.tokens = (int)std::min(chunk, tokens - t0);
         a.x = (const char*)x + t0 * ldx * 2;

@@ -35,7 +35,8 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
 // Four waves a workgroup: with eight, a kernel past 128 registers leaves a CU one workgroup (24 bf16 tokens 243 us, 222
-// with four and 237 with two; one token of eight experts 4096 x 1536 in 8 bits 46, 43 and 48).
+// with four, 237 with two; one token of eight 8-bit experts, of 4096 x 1536 46, 43 and 48, of 2048 x 1024 24, 22 and 27;
+// 58 tokens of eleven 46 with eight and 37 with four).
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kUpRows = 16;
 

@@ -195,7 +195,27 @@ std::map<std::pair<int, void*>, Workspace> g_ws;  // (device, stream) -> workspa
 // the calling path).
 std::vector<std::pair<int, void*>> g_retired;  // (device, pointer)
 
-thread_local std::string t_last_plan;
+// The text of tcm_last_plan: assigned, or (the short calls, which would spend
+// more on it than on their checks) values that are formatted when asked for.
+struct PlanText {
+    std::string s;
+    PlanFormat format = nullptr;
+    int64_t v[kPlanValues];
+    PlanText& operator=(std::string t) {
+        s = std::move(t);
+        format = nullptr;
+        return *this;
+    }
+    const std::string& text() {
+        if (format) {
+            char buf[256];
+            format(buf, sizeof buf, v);
+            *this = std::string(buf);
+        }
+        return s;
+    }
+};
+thread_local PlanText t_last_plan;
 
 // Scratch of tcm_gemm_noalloc: the Stream-K partial tiles (two slots per
 // workgroup of the grid) and the split tiles' arrival counters, in one
@@ -522,6 +542,10 @@ int workspace_for(void* stream, int64_t bytes, void** out) {
     return st;
 }
 void set_last_plan(const char* text) { t_last_plan = text; }
+void set_last_plan(PlanFormat format, std::initializer_list<int64_t> v) {
+    std::copy(v.begin(), v.begin() + std::min<size_t>(v.size(), kPlanValues), t_last_plan.v);
+    t_last_plan.format = format;
+}
 
 }  // namespace tcm
 
@@ -677,7 +701,7 @@ int tcm_tile_order(int32_t t, int32_t tiles_m, int32_t tiles_n, int32_t* tm, int
 }
 
 int tcm_last_plan(char* buf, int64_t len) {
-    const std::string& s = t_last_plan;
+    const std::string& s = t_last_plan.text();
     if (buf && len > 0) {
         int64_t n = std::min<int64_t>(len - 1, (int64_t)s.size());
         memcpy(buf, s.data(), (size_t)n);
@@ -1315,7 +1339,7 @@ int tcm_tune(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
     const int cs = c_elem_bytes(p.c_type);
     p.aligned = ((uintptr_t)A % 16 == 0) && ((uintptr_t)B % 16 == 0) && ((uintptr_t)C % 16 == 0) &&
                 (!use_bias || (uintptr_t)bias % 16 == 0) && ((uintptr_t)C % cs == 0);
-    if (strstr(t_last_plan.c_str(), "kernel=generic")) return TCM_OK;  // the generic kernel: nothing to choose
+    if (strstr(t_last_plan.text().c_str(), "kernel=generic")) return TCM_OK;  // the generic kernel: nothing to choose
     hipStream_t s = (hipStream_t)stream;
     hipEvent_t e0, e1;
     if (hipEventCreate(&e0) != hipSuccess) return TCM_ERR_HIP;
@@ -1333,7 +1357,7 @@ int tcm_tune(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
     auto time_cand = [&](const Cand& c, double* us, int64_t* tiles) -> bool {
         t_cand = &c;
         st = run();  // warm-up, and the plan this candidate really gets
-        const std::string plan = t_last_plan;
+        const std::string plan = t_last_plan.text();
         const int pm = strstr(plan.c_str(), "mode=streamk") ? 2 : 1;
         const bool wide = strstr(plan.c_str(), "kernel=gemv") && strstr(plan.c_str(), " b_col=0 mfma=16x16x32");
         const bool as_asked = c.config == kGemvCand       ? strstr(plan.c_str(), "kernel=gemv") && !wide
