@@ -150,7 +150,14 @@ __device__ __forceinline__ void load8(float (&v)[8], const char* p, int64_t n) {
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? load_float<XT>(p, j) : 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        if (n > 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // (values past the row read its last)
+                const float x = load_float<XT>(p, min(j, (int)n - 1));
+                v[j] = j < n ? x : 0.f;
+            }
+        }
     }
 }
 

@@ -114,6 +114,7 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         int per_cu;
         double lone, shared, lone_wide, shared_wide;
     } kStep[kNumFp8Tiles] = {{1, 1.45, 1.9, 0, 0}, {1, 0.78, 1.04, 1.7, 2.15}, {2, 0.78, 1.17, 1.2, 2.3}, {2, 0.47, 0.73, 0.81, 1.28}};
+    constexpr int64_t kMaxWgs = (int64_t)1 << 22;  // (a launch counts its threads in 32 bits)
     constexpr double kFixed = 3.0, kSum = 2.5, kShare = 0.08, kBytesPerUs = 5e6;
     Fp8Plan best{kFp8Generic, 1};
     if (!fp8_tiles_fit(a) || o.fp8_config == kFp8Generic) return best;
@@ -133,6 +134,7 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
             if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
             const int64_t wgs = tiles * s, rest = wgs % slots;
+            if (wgs >= kMaxWgs) break;
             const double step = (double)(wgs / slots) * shared + (rest == 0 ? 0 : lone + (shared - lone) * (double)rest / (double)slots);
             const double time = kFixed + std::max((double)((steps + s - 1) / s) * step, memory) +
                                 (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
@@ -147,6 +149,7 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         const double round = kRound[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
         for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
             if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
+            if (wgs * s >= kMaxWgs) break;
             const double time = kFixed + std::max((double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round, memory) +
                                 (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t) best_t = time, best = {kFp8Skinny, s};
@@ -221,7 +224,6 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
     const Fp8Tile t = skinny ? Fp8Tile{(int)((M + blocks_m * 16 - 1) / (blocks_m * 16)) * 16, kFp8SkinnyCols, 1, 1, 0, true}
                              : kFp8Tiles[pl.config];
     const int64_t tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
-    if (tm * tn * pl.split >= ((int64_t)1 << 22)) return TCM_ERR_NOT_SUPPORTED;
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
     a.group_m = 4;
