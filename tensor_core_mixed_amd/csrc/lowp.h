@@ -99,7 +99,8 @@ struct MoeArgs {
     void* out;             // [tokens][hidden], x's type
     int64_t ldo;
     int tokens, hidden, inter, experts, topk;
-    void* ws;              // h, the products between the matrices: [pair][inter] binary32
+    void* ws;              // h, the products between the matrices: [pair][inter] binary32,
+                           // or [pair][upper, lower][inter] bfloat16 parts
     // the tiled kernels
     float* y;              // [pair][hidden]
     unsigned* hmax;        // float16 weights: |h|'s largest of each 16, [pair][inter / 16]

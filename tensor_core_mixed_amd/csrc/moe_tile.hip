@@ -17,10 +17,10 @@
 // from 17.9 to 17.3 us and four tokens from 47.5 to 48.6.)
 //
 // 8-bit weights are taken to 16-bit floats (exactly) and a 128-wide block's
-// sums scaled by its tile's scale.  h is binary32 in memory and goes to the
-// matrix cores as the sum of two 16-bit parts: in bfloat16 a remainder of
-// 2^-17, in float16 (float16 weights) after a power of two that brings the
-// pair's largest |h| to 2^14 .. 2^15, 2^-22 of it or better.
+// sums scaled by its tile's scale.  h goes to the matrix cores as the
+// sum of two 16-bit parts: in bfloat16 a remainder of 2^-17; with float16
+// weights it is binary32 in memory and taken to float16 after a power of two
+// that brings the pair's largest |h| to 2^14 .. 2^15, 2^-22 of it or better.
 #include <hip/hip_runtime.h>
 
 #include "fp8_util.h"
@@ -251,7 +251,15 @@ struct Up {
             const bool live = c < n && i0 + i < a.inter;
             const int p = list[min(c, n - 1)];
             const float h = live ? weight[o] * (g / (1.f + expf(-g)) * u) : 0.f;
-            if (live) ((float*)a.ws)[(int64_t)p * a.inter + i0 + i] = h;
+            if constexpr (XT == F16 && !W8) {
+                if (live) ((float*)a.ws)[(int64_t)p * a.inter + i0 + i] = h;
+            } else if (live) {  // both parts at once: the products would take them apart for every 64 rows of W2
+                const __bf16 hi = (__bf16)h;
+                const float rest = h - (float)hi;
+                __bf16* o = (__bf16*)a.ws + 2 * (int64_t)p * a.inter + i0 + i;
+                o[0] = hi;
+                o[a.inter] = (__bf16)(rest == rest ? rest : 0.f);  // (an infinity has no remainder)
+            }
             if constexpr (XT == F16 && !W8) {
                 unsigned m = __builtin_bit_cast(unsigned, h) & 0x7fffffffu;
                 for (int d = 8; d; d >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, d));
@@ -278,29 +286,21 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 
 // ----------------------------------------------------------------- down
 
-// 16-bit parts of eight values times f: v = hi + lo
-template <int HT>
-__device__ __forceinline__ void split8(const f4 (&v)[2], float f, i4& hi, i4& lo) {
+// float16 parts of eight values times f: v = hi + lo
+__device__ __forceinline__ void split8(const i4 (&v)[2], float f, i4& hi, i4& lo) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        const float x = v[d >> 1][2 * (d & 1)] * f, y = v[d >> 1][2 * (d & 1) + 1] * f;
-        if constexpr (HT == F16) {
-            const f16x2_t h = {(_Float16)x, (_Float16)y};
-            const float dx = x - (float)h[0], dy = y - (float)h[1];
-            const f16x2_t l = {(_Float16)(dx == dx ? dx : 0.f), (_Float16)(dy == dy ? dy : 0.f)};  // (infinities have no remainder)
-            hi[d] = __builtin_bit_cast(int, h);
-            lo[d] = __builtin_bit_cast(int, l);
-        } else {
-            const b2 h = {(__bf16)x, (__bf16)y};
-            const float dx = x - (float)h[0], dy = y - (float)h[1];
-            const b2 l = {(__bf16)(dx == dx ? dx : 0.f), (__bf16)(dy == dy ? dy : 0.f)};
-            hi[d] = __builtin_bit_cast(int, h);
-            lo[d] = __builtin_bit_cast(int, l);
-        }
+        const f4 q = __builtin_bit_cast(f4, v[d >> 1]);
+        const float x = q[2 * (d & 1)] * f, y = q[2 * (d & 1) + 1] * f;
+        const f16x2_t h = {(_Float16)x, (_Float16)y};
+        const float dx = x - (float)h[0], dy = y - (float)h[1];
+        const f16x2_t l = {(_Float16)(dx == dx ? dx : 0.f), (_Float16)(dy == dy ? dy : 0.f)};  // (infinities have no remainder)
+        hi[d] = __builtin_bit_cast(int, h);
+        lo[d] = __builtin_bit_cast(int, l);
     }
 }
 
-// Row tiles of W2 a workgroup: h is split into its 16-bit parts once for four (with two, 8% slower).
+// Row tiles of W2 a workgroup (with two, 8% slower).
 constexpr int kDownTiles = 4, kDownRows = 16 * kDownTiles;
 
 // A step is 32 k (8-bit weights: 64 k): 16 bytes of a row a lane.
@@ -310,13 +310,20 @@ struct Down {
     static constexpr int kAhead = 1;
     struct Step {
         i4 w[kDownTiles];
-        f4 h[MT][KV][2];
+        i4 h[MT][KV][2];  // eight k: binary32, or the two bfloat16 parts
         float s;
     };
     struct Src {
         const char* w[kDownTiles];
-        const float *h[MT], *s;
+        const char* h[MT];
+        const float* s;
     };
+    // Chunk v of the step's h from k on, in the pair's 4 * inter bytes: four binary32 values, or eight of the row of upper
+    // (v even) or lower parts; and the bytes left of it.
+    __device__ __forceinline__ static int64_t h_offset(const MoeArgs& a, int k, int v) {
+        return HT == F16 ? (int64_t)(k + 4 * v) * 4 : (int64_t)((v & 1) * (int64_t)a.inter + k + 8 * (v >> 1)) * 2;
+    }
+    __device__ __forceinline__ static int64_t h_left(int64_t left, int v) { return HT == F16 ? (left - 4 * v) * 4 : (left - 8 * (v >> 1)) * 2; }
     // step kt, whole or (PART) the row's last
     template <bool PART>
     __device__ __forceinline__ static void load(Step& t, const Src& s, const MoeArgs& a, int kt, int lane) {
@@ -328,7 +335,7 @@ struct Down {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int v = 0; v < 2 * KV; ++v) t.h[i][v >> 1][v & 1] = __builtin_bit_cast(f4, load16((const char*)(s.h[i] + k + 4 * v)));
+                for (int v = 0; v < 2 * KV; ++v) t.h[i][v >> 1][v & 1] = load16(s.h[i] + h_offset(a, k, v));
         } else {
             const int64_t left = a.inter - k;
 #pragma unroll
@@ -337,7 +344,7 @@ struct Down {
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int v = 0; v < 2 * KV; ++v)
-                    t.h[i][v >> 1][v & 1] = __builtin_bit_cast(f4, load16_part((const char*)(s.h[i] + k + 4 * v), (left - 4 * v) * 4));
+                    t.h[i][v >> 1][v & 1] = load16_part(s.h[i] + h_offset(a, k, v), h_left(left, v));
         }
         if constexpr (W8) t.s = s.s[kt >> 1];
     }
@@ -346,7 +353,10 @@ struct Down {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int v = 0; v < KV; ++v) split8<HT>(t.h[i][v], f[i], hi[i][v], lo[i][v]);
+            for (int v = 0; v < KV; ++v) {
+                if constexpr (HT == F16) split8(t.h[i][v], f[i], hi[i][v], lo[i][v]);
+                else hi[i][v] = t.h[i][v][0], lo[i][v] = t.h[i][v][1];
+            }
 #pragma unroll
         for (int j = 0; j < kDownTiles; ++j) {
             if constexpr (W8) {
@@ -395,7 +405,7 @@ struct Down {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int c = min(16 * i + (lane & 15), n - 1);
-            s.h[i] = (const float*)a.ws + (int64_t)list[c] * a.inter;
+            s.h[i] = (const char*)a.ws + (int64_t)list[c] * a.inter * 4;
             f[i] = kPower ? 1.f / power[c] : 1.f;
         }
         f4 acc[kDownTiles][MT];
