@@ -57,7 +57,7 @@ struct Skinny {
         const int64_t k = kt * 128 + 16 * (lane >> 4);  // (four lanes read 64 consecutive bytes)
         if (kt * 128 + 128 <= a.K) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) x.b[q] = __builtin_nontemporal_load((const i4*)(s.b + k + 64 * q));
+            for (int q = 0; q < 2; ++q) x.b[q] = *(const i4*)(s.b + k + 64 * q);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
