@@ -6,8 +6,10 @@
 // order.  A wave reads 16 rows of B by 128 bytes (32 bytes a lane) and the
 // same k of A's rows (from the caches), takes both to 16-bit floats, which
 // hold them exactly, and multiplies on 16x16x32 MFMAs; the blocks' sums are
-// scaled and added in binary32.  The loads of the next kAhead blocks are in
-// flight while one is multiplied.
+// scaled and added in binary32.  One block a wave is in flight: the waves of
+// two or more workgroups a CU cover the rest (with two or four blocks a wave
+// 16 rows of 4096 x 4096 took 7.3 and 7.7 us, with one 7.1; 37 of 5120 x 8192
+// 33 and 30).
 //
 // Few columns leave CUs without work: k is then cut into `split` ranges, one
 // a workgroup, whose sums a second launch adds in order.
@@ -42,7 +44,6 @@ __device__ __forceinline__ i4 load16(const unsigned char* p, int64_t k, int64_t 
 
 template <bool A5, bool B5, bool BROW, int MT>
 struct Skinny {
-    static constexpr int kAhead = MT <= 2 ? 4 : 2;
     struct Block {
         i4 b[2], a[MT][2];
         float sa[MT];
@@ -120,20 +121,12 @@ struct Skinny {
         f4 acc[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
-        Block x[kAhead];
+        Block x;
         int64_t kt = k_lo + wave;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (kt + u * kWaves < k_hi) load(x[u], s, a, kt + u * kWaves, lane);
-        while (kt < k_hi) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (kt < k_hi) {
-                    multiply(acc, x[u]);
-                    if (kt + kAhead * kWaves < k_hi) load(x[u], s, a, kt + kAhead * kWaves, lane);
-                }
-                kt += kWaves;
-            }
+        if (kt < k_hi) load(x, s, a, kt, lane);
+        for (; kt < k_hi; kt += kWaves) {
+            multiply(acc, x);
+            if (kt + kWaves < k_hi) load(x, s, a, kt + kWaves, lane);
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];

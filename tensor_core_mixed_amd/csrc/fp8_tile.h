@@ -86,23 +86,53 @@ __device__ __forceinline__ f4 mma(const Operand<WIDE>& b, const Operand<WIDE>& a
     }
 }
 
+// E consecutive columns n .. of rows of C
+template <int E>
 struct Epilogue {
-    // E consecutive columns n .. of row m: v += bias and C's contents, ReLU, stored in C's type
-    template <int E>
-    __device__ __forceinline__ static void row(const Fp8Args& a, float (&v)[E], int64_t m, int64_t n) {
-        const bool full = n + E <= a.N;
+    const Fp8Args& a;
+    int64_t n;
+    bool full;  // all of them exist
+    float bias[E];
+
+    __device__ __forceinline__ Epilogue(const Fp8Args& a, int64_t n) : a(a), n(n), full(n + E <= a.N) {
         if (a.has_bias) {
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (full || n + j < a.N) v[j] += load_float<F32>((const char*)a.bias, n + j);
+            for (int j = 0; j < E; ++j) bias[j] = a.bias[min(n + j, a.N - 1)];
         }
-        char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
-        const int cs = c_elem_bytes(a.c_type);
-        if (a.accum) {
+    }
+    // v += row m of C
+    __device__ __forceinline__ void add_c(float (&v)[E], const char* c) const {
+        if (full && a.c_vec) {
+            if (a.c_type == C_ACC) {
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (full || n + j < a.N) v[j] += load_c_any(c + j * cs, a.c_type);
+                for (int q = 0; q < E / 4; ++q) {
+                    const f4 x = *(const f4*)(c + 16 * q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[4 * q + i] += x[i];
+                }
+            } else {
+                unsigned w[E / 2];
+                __builtin_memcpy(w, __builtin_assume_aligned(c, E >= 8 ? 16 : 8), 2 * E);
+#pragma unroll
+                for (int q = 0; q < E; ++q) {
+                    const unsigned short h = (unsigned short)(w[q >> 1] >> (16 * (q & 1)));
+                    v[q] += a.c_type == C_F16 ? (float)__builtin_bit_cast(_Float16, h) : __builtin_bit_cast(float, (unsigned)h << 16);
+                }
+            }
+        } else {
+            const int cs = c_elem_bytes(a.c_type);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += load_c_any(c + min<int64_t>(j, a.N - 1 - n) * cs, a.c_type);
         }
+    }
+    // v + bias + C's contents, ReLU, stored in C's type as row m
+    __device__ __forceinline__ void store(float (&v)[E], int64_t m) const {
+        char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
+        if (a.has_bias) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += bias[j];
+        }
+        if (a.accum) add_c(v, c);
         if (a.relu) {
 #pragma unroll
             for (int j = 0; j < E; ++j) v[j] = v[j] > 0.f ? v[j] : 0.f;
@@ -128,6 +158,7 @@ struct Epilogue {
                 __builtin_memcpy(__builtin_assume_aligned(c, E >= 8 ? 16 : 8), w, 2 * E);
             }
         } else {
+            const int cs = c_elem_bytes(a.c_type);
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 if (n + j < a.N) store_c_any(c + j * cs, a.c_type, v[j]);
@@ -491,14 +522,16 @@ struct Tile {
             return;
         }
         const int64_t n = n0 + wn * 64 + 16 * (lane >> 4);
+        if (n >= a.N) return;
+        const Epilogue<16> epi(a, n);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int64_t m = m0 + wm * TM + 16 * i + (lane & 15);
-            if (m >= a.M || n >= a.N) continue;
+            if (m >= a.M) continue;
             float v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = acc[i][e >> 2][e & 3];
-            Epilogue::row<16>(a, v, m, n);
+            epi.store(v, m);
         }
     }
 
@@ -530,8 +563,9 @@ struct Tile {
             for (int u = 0; u < 8; ++u)
                 if (k + u < a.split) s += x[u];
         }
+        const Epilogue<4> epi(a, n);
         float v[4] = {s[0], s[1], s[2], s[3]};
-        Epilogue::row<4>(a, v, m, n);
+        epi.store(v, m);
     }
 };
 

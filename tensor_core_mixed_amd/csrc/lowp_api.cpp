@@ -143,7 +143,7 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
     }
     // Few rows: a workgroup's waves take a block each at a time, rows cost reads of A from the caches.
     if (forced < 0 ? a.M <= kFp8SkinnyRows : forced == kFp8Skinny) {
-        static constexpr double kRound[4] = {0.9, 1.4, 1.9, 2.9};
+        static constexpr double kRound[4] = {0.87, 1.4, 1.75, 2.6};
         const int64_t blocks_m = (a.M + kFp8SkinnyRows - 1) / kFp8SkinnyRows;
         const int64_t wgs = blocks_m * ((a.N + kFp8SkinnyCols - 1) / kFp8SkinnyCols);
         const double round = kRound[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
