@@ -14,9 +14,11 @@
 //
 // The MFMA takes its A operand from B's rows and its B operand from A's, so a
 // lane's accumulators run along n at one m: sa is one value a lane and tile,
-// and stores are contiguous.  B's rows are dealt to the 16-row tiles of a
-// wave's 64 columns as n = 16 * (i / 4) + 4 * tile + i % 4: a lane then holds
-// 16 consecutive columns of a row.  (Which k an operand register holds plays
+// and a row's stores are contiguous: row i of a wave's tiles j = 0 .. 3 is
+// column 16 (i / 4) + 4 j + i % 4 of its 64 for 16-bit C (16 columns, 32 bytes
+// a lane) and 16 j + i for binary32 C (four lanes write 64 bytes together:
+// 8039x7376x1504 225 us, 248 with the other order; 16-bit C was 1% slower).
+// (Which k an operand register holds plays
 // no part as long as both operands agree.)
 //
 // Copies, LDS layout and pipeline are the dense kernels': 128-byte rows of
@@ -182,11 +184,14 @@ struct Tile {
     static constexpr int LDS = NST * STAGE;
     static_assert(LDS <= 160 * 1024 && BM <= 256 && BN <= 256, "");
 
-    // Row i of the 16 that a fragment read takes is row i of A's tile, and of B's 16 * (i / 4) + 4 * tile + i % 4; both
-    // swizzles are i / 2 % 8: any sixteen lanes that the LDS serves at once (0-3, 12-15, 20-27 and their complements,
-    // by the counters) then fall on distinct banks.  (With i % 8 ^ i / 8 for A every read of A took twice its time.)
+    // The column of the wave's 64 that is row i of its tile j, and its parts: n_row(i) + n_tile(j).
+    __device__ __forceinline__ static constexpr int n_row(int i) { return WIDE ? i : 16 * (i >> 2) + (i & 3); }
+    __device__ __forceinline__ static constexpr int n_tile(int j) { return (WIDE ? 16 : 4) * j; }
+    // Both swizzles of the row that a fragment read takes as its i-th are i / 2 % 8: any sixteen lanes that the LDS serves
+    // at once (0-3, 12-15, 20-27 and their complements, by the counters) then fall on distinct banks.  (With i % 8 ^ i / 8
+    // for A every read of A took twice its time.)
     __device__ __forceinline__ static int swz_a(int r) { return (r >> 1) & 7; }
-    __device__ __forceinline__ static int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 4) & 3) << 1; }
+    __device__ __forceinline__ static int swz_b(int r) { return WIDE ? (r >> 1) & 7 : ((r >> 1) & 1) | ((r >> 4) & 3) << 1; }
 
     // A wave's copies of a step: IA of A, IB of B, and of the scales one (eight waves: 0-3 A's and 4-7 B's) or two.
     static constexpr int NS = NW == 4 ? 2 : 1, OPS = IA + IB + NS;
@@ -336,12 +341,12 @@ struct Tile {
         }
     }
     __device__ __forceinline__ static void read_col(Cols& f, const lds_char* s, const Lane& l, int j) {
-        f.b[j] = read_pair(s, l.b[0] + j * 512, l.b[1] + j * 512);
+        f.b[j] = read_pair(s, l.b[0] + n_tile(j) * 128, l.b[1] + n_tile(j) * 128);
     }
     __device__ __forceinline__ static void read_scales(Cols& f, const lds_char* s, const Lane& l) {
         if constexpr (BROW) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f.s[j] = *(const __attribute__((address_space(3))) f4*)(s + l.sb + 16 * j);
+            for (int j = 0; j < 4; ++j) f.s[j] = *(const __attribute__((address_space(3))) f4*)(s + l.sb + 4 * n_tile(j));
         } else {
             f.s[0][0] = lds_f(s, l.sb);
         }
@@ -458,14 +463,14 @@ struct Tile {
         Lane l;
         {
             const int i = lane & 15, g = lane >> 4;
-            const int ra = wm * TM + i, rb = wn * 64 + 16 * (i >> 2) + (i & 3);
+            const int ra = wm * TM + i, rb = wn * 64 + n_row(i);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 l.a[q] = ra * 128 + (((g + 4 * q) ^ swz_a(ra)) << 4);
                 l.b[q] = A_BYTES + rb * 128 + (((g + 4 * q) ^ swz_b(rb)) << 4);
             }
             l.sa = SA_OFF + ra * 4;
-            l.sb = SB_OFF + (wn * 64 + (BROW ? 16 * g : 0)) * 4;
+            l.sb = SB_OFF + (wn * 64 + (BROW ? n_row(4 * g) : 0)) * 4;
         }
         // the step that needs mask_tail is the matrix's last
         const int last = (int)((a.K + 127) / 128) - 1, k_tail = (a.K & 15) && last < k_hi ? (int)(a.K & 127) : 0;
@@ -521,21 +526,28 @@ struct Tile {
                 for (int j = 0; j < 4; ++j) o[(i * 4 + j) * 64] = acc[i][j];
             return;
         }
-        const int64_t n = n0 + wn * 64 + 16 * (lane >> 4);
-        if (n >= a.N) return;
-        const Epilogue<16> epi(a, n);
+        store_tile(acc, a, m0 + wm * TM + (lane & 15), n0 + wn * 64 + n_row(4 * (lane >> 4)));
+    }
+    // accumulators to C: row m of row tile 0, column n of tile 0
+    __device__ __forceinline__ static void store_tile(const f4 (&acc)[FM][4], const Fp8Args& a, int64_t m, int64_t n) {
+        constexpr int E = WIDE ? 4 : 16;  // consecutive columns a lane has
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int64_t m = m0 + wm * TM + 16 * i + (lane & 15);
-            if (m >= a.M) continue;
-            float v[16];
+        for (int q = 0; q < 16 / E; ++q) {
+            const int64_t nq = n + n_tile(q);
+            if (nq >= a.N) continue;
+            const Epilogue<E> epi(a, nq);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = acc[i][e >> 2][e & 3];
-            epi.store(v, m);
+            for (int i = 0; i < FM; ++i) {
+                if (m + 16 * i >= a.M) continue;
+                float v[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = acc[i][(q * E + e) >> 2][e & 3];
+                epi.store(v, m + 16 * i);
+            }
         }
     }
 
-    // Sum of a split launch: a wave takes one accumulator tile (16 rows by four columns a lane) and has up to eight
+    // Sum of a split launch (of either width): a wave takes one accumulator tile (16 rows by four columns a lane) and has up to eight
     // shares' partials of it in flight (one after the other, eleven shares of 37 rows took 6.3 us); they are added in
     // order.
     __device__ __forceinline__ static void run_sum(const Fp8Args& a) {
@@ -549,7 +561,7 @@ struct Tile {
         int tm, tn;
         super_order(t, a.tiles_m, a.tiles_n, a.group_m, a.super_m, a.super_n, &tm, &tn);
         const int wm = wave / WN, wn = wave % WN;
-        const int64_t m = (int64_t)tm * BM + wm * TM + 16 * i + (lane & 15), n = (int64_t)tn * BN + wn * 64 + 16 * (lane >> 4) + 4 * j;
+        const int64_t m = (int64_t)tm * BM + wm * TM + 16 * i + (lane & 15), n = (int64_t)tn * BN + wn * 64 + (a.c_type == C_ACC ? 4 * (lane >> 4) + 16 * j : 16 * (lane >> 4) + 4 * j);
         if (m >= a.M || n >= a.N) return;
         const f4* p = (const f4*)a.ws + ((((int64_t)t * NW + wave) * FM + i) * 4 + j) * 64 + lane;
         const int64_t step = T * NW * FM * 4 * 64;
