@@ -101,11 +101,12 @@ bool fp8_tiles_fit(const Fp8Args& a) {
            !(a.ldb & 15) && a.lda < lim && a.ldb < lim && a.ldsb < ((int64_t)1 << 26);
 }
 // The macro tile and the k ranges of a product by a model of its time, in
-// microseconds: a workgroup's K-steps, whose time grows from `lone` to
-// `shared` as the chip fills; the operands' way from memory at least; and for
-// a split the sum's launch and the partial tiles' way through the caches.
-// Fitted to products of 37 to 8192 rows, 8-bit and (binary32 C) 16-bit
-// operands.
+// microseconds: the launch; for every round of workgroups a fill of its
+// pipelines and its K-steps, whose time grows from `lone` to `shared` as the
+// chip fills, or the operands' way from memory where that is longer; C's or
+// the partial tiles' way out; and for a split the sum's launch, each share's
+// part of it and the partial tiles' way back.  Fitted to products of 37 to
+// 8192 rows, 8-bit and (binary32 C) 16-bit operands.
 struct Fp8Plan {
     int config, split;
 };
@@ -113,9 +114,9 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
     static constexpr struct {
         int per_cu;
         double lone, shared, lone_wide, shared_wide;
-    } kStep[kNumFp8Tiles] = {{1, 1.45, 1.9, 0, 0}, {1, 0.78, 1.04, 1.7, 2.15}, {2, 0.78, 1.17, 1.2, 2.3}, {2, 0.47, 0.73, 0.81, 1.28}};
+    } kStep[kNumFp8Tiles] = {{1, 1.28, 1.65, 0, 0}, {1, 0.66, 0.93, 1.6, 1.83}, {2, 0.69, 1.04, 1.2, 2.13}, {2, 0.38, 0.63, 0.75, 1.19}};
     constexpr int64_t kMaxWgs = (int64_t)1 << 22;  // (a launch counts its threads in 32 bits)
-    constexpr double kFixed = 3.0, kSum = 2.5, kShare = 0.08, kBytesPerUs = 5e6;
+    constexpr double kFixed = 3.0, kRound = 3.0, kSum = 2.5, kShare = 0.25, kBytesPerUs = 5e6;
     Fp8Plan best{kFp8Generic, 1};
     if (!fp8_tiles_fit(a) || o.fp8_config == kFp8Generic) return best;
     const bool wide = a.c_type == C_ACC;
@@ -136,17 +137,19 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
             const int64_t wgs = tiles * s, rest = wgs % slots;
             if (wgs >= kMaxWgs) break;
             const double step = (double)(wgs / slots) * shared + (rest == 0 ? 0 : lone + (shared - lone) * (double)rest / (double)slots);
-            const double time = kFixed + std::max((double)((steps + s - 1) / s) * step, memory) +
-                                (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            const double rounds = (double)((wgs + slots - 1) / slots);
+            const double out = (double)wgs * t.bm * t.bn * (s > 1 ? 4 : c_elem_bytes(a.c_type)) / kBytesPerUs;
+            const double time = kFixed + std::max(rounds * kRound + (double)((steps + s - 1) / s) * step, memory) + out +
+                                (s > 1 ? kSum + kShare * s + 4.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t) best_t = time, best = {c, s};
         }
     }
     // Few rows: a workgroup's waves take a block each at a time, rows cost reads of A from the caches.
     if (forced < 0 ? a.M <= kFp8SkinnyRows : forced == kFp8Skinny) {
-        static constexpr double kRound[4] = {0.87, 1.4, 1.75, 2.6};
+        static constexpr double kBlock[4] = {0.87, 1.4, 1.75, 2.6};
         const int64_t blocks_m = (a.M + kFp8SkinnyRows - 1) / kFp8SkinnyRows;
         const int64_t wgs = blocks_m * ((a.N + kFp8SkinnyCols - 1) / kFp8SkinnyCols);
-        const double round = kRound[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
+        const double round = kBlock[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
         for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
             if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
             if (wgs * s >= kMaxWgs) break;
