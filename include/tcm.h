@@ -501,8 +501,9 @@ const char* tcm_status_string(int status);
  *                  (column-major B) (1..4096).
  *   "fp8_config"   tcm_gemm_fp8's kernel: -1 = planner decides, 0 .. 3 = the
  *                  256x256, 256x128, 128x128 or 64x128 tile (f32 C: not the
- *                  first), 4 = the few-rows kernel, 5 = the any-alignment
- *                  kernel; a kernel that cannot serve the call is ignored.
+ *                  first; another tile serves it), 4 = the few-rows kernel, 5 =
+ *                  the any-alignment kernel, which also serves what the
+ *                  kernel given cannot.
  *   "fp8_split"    0 = planner decides, else the k ranges each of its tiles
  *                  is cut into (1..64, at most one a 128-wide block).
  * Unknown keys or out-of-range values: TCM_ERR_INVALID_VALUE.

@@ -124,7 +124,7 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
     const double memory = (double)(a.M + a.N) * (double)a.K / kBytesPerUs;
     double best_t = 1e30;
     int forced = o.fp8_config;
-    if (forced >= 0 && forced < kNumFp8Tiles && wide && !kFp8Tiles[forced].wide) forced = -1;  // cannot serve
+    if (forced >= 0 && forced < kNumFp8Tiles && wide && !kFp8Tiles[forced].wide) forced = -1;  // (cannot serve: another tile does)
     for (int c = 0; c < kNumFp8Tiles; ++c) {
         const Fp8Tile& t = kFp8Tiles[c];
         if (wide && !t.wide) continue;
@@ -145,7 +145,7 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         }
     }
     // Few rows: a workgroup's waves take a block each at a time, rows cost reads of A from the caches.
-    if (forced < 0 ? a.M <= kFp8SkinnyRows : forced == kFp8Skinny) {
+    if (o.fp8_config < 0 ? a.M <= kFp8SkinnyRows : o.fp8_config == kFp8Skinny) {
         static constexpr double kBlock[4] = {0.87, 1.4, 1.75, 2.6};
         const int64_t blocks_m = (a.M + kFp8SkinnyRows - 1) / kFp8SkinnyRows;
         const int64_t wgs = blocks_m * ((a.N + kFp8SkinnyCols - 1) / kFp8SkinnyCols);
