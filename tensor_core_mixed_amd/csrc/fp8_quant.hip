@@ -23,6 +23,9 @@
 // element, no branch (settling ties as above took three quarters of the waves
 // there: 8192^2 bf16 both ways 69 us).
 //
+// 8192^2 bf16 both ways takes 61.5 us and 4096 x 11008 f32 tiles both ways 53.9:
+// 4.4 and 5.0 TB/s, bound by memory (a copy moves 4.86).
+//
 // NaN and infinity follow the formula: a block that holds a NaN has a NaN
 // scale and all q NaN; one with an infinity (and no NaN) has an infinite
 // scale, finite x become 0 and the infinities NaN.

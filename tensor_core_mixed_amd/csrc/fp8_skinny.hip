@@ -9,7 +9,8 @@
 // scaled and added in binary32.  One block a wave is in flight: the waves of
 // two or more workgroups a CU cover the rest (with two or four blocks a wave
 // 16 rows of 4096 x 4096 took 7.3 and 7.7 us, with one 7.1; 37 of 5120 x 8192
-// 33 and 30).
+// 33 and 30).  One row of 8192 x 8192 takes 16.7 us, 4.0 TB/s; more rows cost
+// their reads of A, every workgroup all of it.
 //
 // Few columns leave CUs without work: k is then cut into `split` ranges, one
 // a workgroup, whose sums a second launch adds in order.

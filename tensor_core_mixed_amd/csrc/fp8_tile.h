@@ -18,14 +18,20 @@
 // column 16 (i / 4) + 4 j + i % 4 of its 64 for 16-bit C (16 columns, 32 bytes
 // a lane) and 16 j + i for binary32 C (four lanes write 64 bytes together:
 // 8039x7376x1504 225 us, 248 with the other order; 16-bit C was 1% slower).
-// (Which k an operand register holds plays
-// no part as long as both operands agree.)
+// (Which k an operand register holds plays no part as long as both operands
+// agree.)
 //
 // Copies, LDS layout and pipeline are the dense kernels': 128-byte rows of
 // each operand go to LDS by 16-byte direct loads, the chunk index XOR-ed with
 // a function of the row so that the reads of a fragment fall on distinct
 // banks; STAGES stages, copies STAGES - 1 steps ahead.  The scales of a step
 // travel with it (4-byte direct loads).
+//
+// 8192^3 takes 460 to 475 us (2.3 to 2.4 PFLOP/s; the matrix cores 61% busy at
+// 1.85 GHz; 348 us without the copies, 448 without the multiply-adds), f32 C
+// 4096x4096x5003 with two row scales 167 us (1.0 PFLOP/s, bound by the vector
+// ALU: a tile's four 16-bit MFMAs come with eight conversions, four products
+// of two scales and four multiply-adds a lane).
 #pragma once
 #include <hip/hip_runtime.h>
 
