@@ -97,3 +97,16 @@ def moe(**kw):
 ])
 def test_moe_refuses(kw, st):
     assert moe(**kw) == st
+
+
+@pytest.mark.parametrize("key,default,allowed,refused", [
+    ("fp8_config", -1, (-1, 0, 3, 4, 5), (-2, 6, 1 << 32)), ("fp8_split", 0, (0, 1, 64), (-1, 65, 1 << 32))])
+def test_options(key, default, allowed, refused):
+    assert T.tcm_get_option(key) == default
+    try:
+        for value in allowed:
+            assert T.tcm_set_option(key, value) == OK and T.tcm_get_option(key) == value
+        for value in refused:
+            assert T.tcm_set_option(key, value) == INV and T.tcm_get_option(key) == allowed[-1]
+    finally:
+        assert T.tcm_set_option(key, default) == OK
