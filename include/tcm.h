@@ -407,8 +407,10 @@ int tcm_gemm_fp8(int64_t M, int64_t N, int64_t K,
  *                (the bias that balances the experts' load).
  *   ids, weights tokens x topk, dense; must not overlap an input.
  * experts <= 1024 and topk <= 64 (else TCM_ERR_NOT_SUPPORTED), topk <=
- * experts.  Keys with a bias are formed in binary64.  A NaN key ranks above
- * every number; a sum of zero (a row of -inf) gives weights of zero; a
+ * experts.  Keys with a bias are formed in binary64.  Scores too small for
+ * binary32 count in full: with TCM_ROUTE_NORM chosen logits of -1000 and
+ * -1001 weigh 0.73 and 0.27, whatever the others are.  A NaN key ranks above
+ * every number; chosen logits that are all -inf give weights of zero; a
  * softmax over NaN or +inf is NaN.  Returns as tcm_quantize_fp8.
  */
 int tcm_moe_route(int64_t tokens, int64_t experts, int64_t topk,

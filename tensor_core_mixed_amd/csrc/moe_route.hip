@@ -7,8 +7,8 @@
 //
 // Both scores rise with x, so without a bias the logits order the experts
 // exactly.  With a bias the keys count in binary64: near ones would change
-// places in 32 bits.  A sum of zero (a row of -inf) gives weights of zero; a
-// NaN key ranks above every number.
+// places in 32 bits.  Chosen scores of zero (a row of -inf) give weights of
+// zero; a NaN key ranks above every number.
 //
 // One wave takes one token, expert e on lane e % 64.  Each pass takes the
 // wave's largest remaining key, as order-preserving 32-bit integers, by a
@@ -17,7 +17,9 @@
 // bias are formed in binary32 first, off by less than half kSlack of the largest
 // score and of the key: a token two of whose topk + 1 first keys lie closer
 // than that is routed again by the binary64 passes, as is one with a NaN or a
-// +inf or whose logits are all -inf.  8192 tokens of 256 experts with a bias,
+// +inf or whose logits are all -inf, or with a chosen score under 2^-100, which
+// binary32 holds in few bits or not at all (normalised weights are ratios, the
+// same however small the scores are).  8192 tokens of 256 experts with a bias,
 // eight chosen, take 10 us, bound by the instructions of the nine passes (25 us
 // by binary64 passes alone).
 #include <hip/hip_runtime.h>
@@ -142,6 +144,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int la
     }
     float w = 0.f;
     if (lane < a.topk) w = a.sigmoid ? 1.f / (1.f + expf(-my_x)) : expf(my_x - mx) * inv;
+    if (__ballot(lane < a.topk && w < 0x1p-100f && my_x > -INFINITY)) return false;
     if (a.norm) {
         const float total = wave_sum(w);
         w = total == 0.f ? 0.f : w / total;
@@ -215,9 +218,22 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
             total += s;
         }
     }
+    double w = my_score;
+    if (a.norm) {
+        w /= total;
+        if (total < 0x1p-900) {
+            // near the end of binary64's range or past it: differences of log-scores (up to a constant) keep the ratios
+            double ls = lane < a.topk ? (double)load_float<XT>(row, my_id) : -INFINITY;
+            if (a.sigmoid) ls = fmin(ls, 0.0) - log1p(exp(-fabs(ls)));
+            double top = ls;
+            for (int o = 32; o; o >>= 1) top = fmax(top, __shfl_xor(top, o));
+            w = top == -INFINITY ? 0.0 : exp(ls - top);
+            total = w;
+            for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
+            w = top == -INFINITY ? 0.0 : w / total;
+        }
+    }
     if (lane < a.topk) {
-        double w = my_score;
-        if (a.norm) w = total == 0 ? 0.0 : w / total;
         a.ids[t * a.topk + lane] = my_id;
         a.weights[t * a.topk + lane] = (float)(w * (double)a.scale);
     }
