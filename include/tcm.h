@@ -26,9 +26,11 @@
  * ready when the stream reaches the call.  Calls on one stream run in order.
  * The library's state is a cached split-k workspace per (device, stream),
  * so concurrent calls on different streams are independent, plus the
- * process-wide switches and tuning table below (mutex-protected).  The
- * workspace grows on demand (hipMalloc, plus a zero-fill kernel for its
- * counters), never synchronising; an outgrown buffer is kept, not freed,
+ * process-wide switches and tuning table below (mutex-protected).  Host
+ * threads may call on one stream at once: launches that hand results on
+ * through its workspace are enqueued with no other call's use of it between
+ * them.  The workspace grows on demand (hipMalloc, plus a zero-fill kernel
+ * for its counters), never synchronising; an outgrown buffer is kept, not freed,
  * until tcm_release_workspace, because kernels or graphs enqueued earlier may
  * still use it.  A call whose plan fits the stream's existing workspace
  * allocates nothing and issues only kernel launches, so it can be captured

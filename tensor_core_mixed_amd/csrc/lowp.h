@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <initializer_list>
+#include <mutex>
 
 namespace tcm {
 
@@ -120,8 +121,9 @@ struct LowpOpts {
 };
 LowpOpts lowp_opts();
 // Shared with the C ABI's other entry points (tcm_api.cpp): the stream's
-// workspace, grown to `bytes` (a tcm_status), and the text of tcm_last_plan.
-int workspace_for(void* stream, int64_t bytes, void** out);
+// workspace, grown to `bytes` (a tcm_status), with the lock to hold until the
+// last launch that uses it, and the text of tcm_last_plan.
+int workspace_for(void* stream, int64_t bytes, void** out, std::unique_lock<std::mutex>* order);
 void set_last_plan(const char* text);
 // (formatted when it is asked for)
 constexpr int kPlanValues = 10;

@@ -232,9 +232,10 @@ int gemm_fp8_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
     a.group_m = 4;
     tile_order_shape(a.tiles_m, a.tiles_n, a.group_m, &a.super_m, &a.super_n);
     a.split = pl.split;
+    std::unique_lock<std::mutex> order;
     if (a.split > 1) {
         void* ws = nullptr;
-        const int st = workspace_for(stream, (skinny ? M * N : tm * tn * t.bm * t.bn) * a.split * 4, &ws);
+        const int st = workspace_for(stream, (skinny ? M * N : tm * tn * t.bm * t.bn) * a.split * 4, &ws, &order);
         if (st != TCM_OK) return st;
         a.ws = (float*)ws;
     }
@@ -339,7 +340,9 @@ int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int
     const int64_t chunk = std::min<int64_t>(tiled ? kMoePairs / topk : ((int64_t)1 << 25) / per_token, tokens);
     if (chunk == 0) return TCM_ERR_NOT_SUPPORTED;
     const int64_t h_bytes = (chunk * a.topk * inter * 4 + 15) & ~(int64_t)15, y_bytes = (chunk * a.topk * hidden * 4 + 15) & ~(int64_t)15;
-    const int st = workspace_for(stream, std::max<int64_t>(tiled ? h_bytes + y_bytes + chunk * topk * ((inter + 15) / 16) * 4 : h_bytes, 4), &a.ws);
+    std::unique_lock<std::mutex> order;
+    const int st = workspace_for(stream, std::max<int64_t>(tiled ? h_bytes + y_bytes + chunk * topk * ((inter + 15) / 16) * 4 : h_bytes, 4), &a.ws,
+                                 &order);
     if (st != TCM_OK) return st;
     a.y = (float*)((char*)a.ws + h_bytes);
     a.hmax = (unsigned*)((char*)a.ws + h_bytes + y_bytes);

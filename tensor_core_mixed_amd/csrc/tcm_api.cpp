@@ -189,6 +189,20 @@ struct Workspace {
     int64_t n_counters = 0;
 };
 std::map<std::pair<int, void*>, Workspace> g_ws;  // (device, stream) -> workspace
+// Held from the look-up of a stream's workspace (or of the fixed scratch) to
+// the last launch of the call: a call of several launches hands its partial
+// results on through it, so another host thread's launches on the same stream
+// must not come between them.  Streams have locks of their own: one stream's
+// full queue holds no other up.  (Taken before g_mu, never after it.)
+std::map<std::pair<int, void*>, std::mutex> g_enqueue;  // (device, stream) -> lock
+std::unique_lock<std::mutex> enqueue_order(int dev, void* stream) {
+    std::mutex* m;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        m = &g_enqueue[{dev, stream}];
+    }
+    return std::unique_lock<std::mutex>(*m);
+}
 // Buffers a workspace outgrew.  A graph captured before the growth still
 // points at them, and kernels enqueued before it may still run on them, so
 // they live until tcm_release_workspace (no free, and no synchronisation, on
@@ -530,13 +544,14 @@ LowpOpts lowp_opts() {
     std::lock_guard<std::mutex> lk(g_mu);
     return g_lowp;
 }
-int workspace_for(void* stream, int64_t bytes, void** out) {
+int workspace_for(void* stream, int64_t bytes, void** out, std::unique_lock<std::mutex>* order) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) {
         (void)hipGetLastError();
         return TCM_ERR_HIP;
     }
     Workspace w;
+    *order = enqueue_order(dev, stream);
     const int st = get_workspace(dev, stream, bytes, 0, &w);
     if (st == TCM_OK) *out = w.partial;
     return st;
@@ -734,6 +749,7 @@ void tcm_release_workspace(void) {
     }
     (void)hipSetDevice(cur);
     g_ws.clear();
+    g_enqueue.clear();
     g_retired.clear();
 }
 
@@ -871,7 +887,9 @@ int gemm_impl(int64_t batch, int64_t M, int64_t N, int64_t K, const void* A, int
         v.a_bytes = a_one;
         v.b_col = p.b_col ? 1 : 0;
         v.wide = pl.gemv_wide ? 1 : 0;
+        std::unique_lock<std::mutex> order;
         if (pl.ws_partial_bytes > 0) {
+            order = enqueue_order(dev, stream);
             if (noalloc) {
                 char* base = nullptr;
                 int st2 = scratch_of(dev, &base);
@@ -926,6 +944,8 @@ int launch_tiled(const Problem& p, const Plan& pl, TileArgs& a, int dev, void* s
     a.sk_fixup_kernel = pl.fixup_kernel ? 1 : 0;
     a.split = pl.split;
     if (pl.split > kMaxSplit) return TCM_ERR_INVALID_VALUE;  // the sum kernel holds at most kMaxSplit partials a block
+    std::unique_lock<std::mutex> order;
+    if (pl.mode == 2 && pl.sk_tiles > 0) order = enqueue_order(dev, stream);
     if (pl.mode == 2 && pl.sk_tiles > 0 && noalloc) {
         char* base = nullptr;
         int st = scratch_of(dev, &base);
@@ -1208,8 +1228,10 @@ int grouped_impl(int64_t count, const tcm_group_entry* ent, int64_t K, int dtype
         tile0 += (int64_t)y.tiles_m * y.tiles_n;
     }
     if (tile0 != pl.tiles) return TCM_ERR_INVALID_VALUE;  // the plan and the table disagree (cannot happen)
+    std::unique_lock<std::mutex> order;
     if (pl.mode == 2 && pl.sk_tiles > 0) {
         Workspace w;
+        order = enqueue_order(dev, stream);
         int ws = get_workspace(dev, stream, pl.ws_partial_bytes, pl.ws_counters, &w);
         if (ws != TCM_OK) return ws;
         a.ws_partial = (float*)w.partial;
