@@ -249,7 +249,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
 
 template <int XT, int NPL>
 int launch_n(const RouteArgs& a, hipStream_t s) {
-    const int64_t per = (int64_t)kWaves << 30;  // tokens per launch
+    const int64_t per = (int64_t)kWaves << 23;  // tokens per launch, which counts its threads in 32 bits
     for (int64_t t = 0; t < a.tokens; t += per) {
         RouteArgs e = a;
         e.tokens = a.tokens - t < per ? a.tokens - t : per;

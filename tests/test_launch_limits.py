@@ -1,0 +1,22 @@
+"""Grids of the largest sizes that the 8-bit product, its quantiser, the router and the expert layer take: a launch counts
+its threads in 32 bits along x and its workgroups in 16 along y."""
+import pytest
+
+import host_util
+
+CHECK = """
+        assert launches()
+        for l in launches():
+            assert 0 < l.grid.x and l.grid.x * l.block.x < 1 << 32, (l.grid.x, l.block.x, T.tcm_last_plan())
+            assert 0 < l.grid.y < 1 << 16 and l.grid.z == 1 and l.block.x <= 1024 and l.block.y == l.block.z == 1
+"""
+
+
+@pytest.mark.parametrize("tokens", [(1 << 26) - 1, 1 << 26, (1 << 26) + 5, 1 << 28, (1 << 35) + 3])
+def test_router(tmp_path, tokens):
+    out = host_util.run(tmp_path, f"""
+        assert T.tcm_moe_route({tokens}, 4, 1, 1 << 44, 4, T.TCM_F16_F32, None, 1.0, 1 << 45, 1 << 46, None) == T.TCM_OK
+        {CHECK}
+        print(sum(l.grid.x for l in launches()))
+    """)
+    assert int(out) == -(-tokens // 4)
