@@ -333,28 +333,30 @@ int launch_x(bool e5m2, bool tile, const QuantArgs& a, hipStream_t s) {
     const bool rows_only = !tile && !a.qt;
     const int64_t high = rows_only ? 16 : 128;
     const int64_t nc = scale_blocks(a.cols), nr = (a.rows + high - 1) / high;
-    // the grid's y extent holds 65535 workgroups: longer matrices go in bands
-    for (int64_t b = 0; b < nr; b += 65535) {
-        QuantArgs e = a;
-        const int64_t r0 = b * high;
-        e.rows = a.rows - r0;
-        e.x = (const char*)a.x + r0 * a.ldx * (XT == F32 ? 4 : 2);
-        if (a.q) e.q = a.q + r0 * a.ldq, e.s = a.s + (tile ? b * a.lds : r0);
-        if (a.qt) e.qt = a.qt + r0, e.st = a.st + (tile ? b : b * a.ldst);
-        const int64_t n = nr - b < 65535 ? nr - b : 65535;
-        if (n * high < e.rows) e.rows = n * high;
-        const dim3 grid((unsigned)nc, (unsigned)n);
-        if (rows_only) {
-            if (e5m2) hipLaunchKernelGGL((quant_row_kernel<XT, true>), grid, dim3(kThreads), 0, s, e);
-            else hipLaunchKernelGGL((quant_row_kernel<XT, false>), grid, dim3(kThreads), 0, s, e);
-        } else if (e5m2) {
-            if (tile) hipLaunchKernelGGL((quant_tile_kernel<XT, true, true>), grid, dim3(kThreads), 0, s, e);
-            else hipLaunchKernelGGL((quant_tile_kernel<XT, true, false>), grid, dim3(kThreads), 0, s, e);
-        } else {
-            if (tile) hipLaunchKernelGGL((quant_tile_kernel<XT, false, true>), grid, dim3(kThreads), 0, s, e);
-            else hipLaunchKernelGGL((quant_tile_kernel<XT, false, false>), grid, dim3(kThreads), 0, s, e);
+    // the grid's y extent holds 65535 workgroups and its x extent 2^32 - 1 threads: larger matrices go in bands
+    constexpr int64_t kWide = (int64_t)1 << 23, kHigh = 65535;
+    for (int64_t b = 0; b < nr; b += kHigh)
+        for (int64_t d = 0; d < nc; d += kWide) {
+            QuantArgs e = a;
+            const int64_t r0 = b * high, c0 = d * kScaleBlock;
+            const int64_t n = nr - b < kHigh ? nr - b : kHigh, m = nc - d < kWide ? nc - d : kWide;
+            e.rows = a.rows - r0 < n * high ? a.rows - r0 : n * high;
+            e.cols = a.cols - c0 < m * kScaleBlock ? a.cols - c0 : m * kScaleBlock;
+            e.x = (const char*)a.x + (r0 * a.ldx + c0) * (XT == F32 ? 4 : 2);
+            if (a.q) e.q = a.q + r0 * a.ldq + c0, e.s = a.s + (tile ? b * a.lds + d : d * a.lds + r0);
+            if (a.qt) e.qt = a.qt + c0 * a.ldqt + r0, e.st = a.st + (tile ? d * a.ldst + b : b * a.ldst + c0);
+            const dim3 grid((unsigned)m, (unsigned)n);
+            if (rows_only) {
+                if (e5m2) hipLaunchKernelGGL((quant_row_kernel<XT, true>), grid, dim3(kThreads), 0, s, e);
+                else hipLaunchKernelGGL((quant_row_kernel<XT, false>), grid, dim3(kThreads), 0, s, e);
+            } else if (e5m2) {
+                if (tile) hipLaunchKernelGGL((quant_tile_kernel<XT, true, true>), grid, dim3(kThreads), 0, s, e);
+                else hipLaunchKernelGGL((quant_tile_kernel<XT, true, false>), grid, dim3(kThreads), 0, s, e);
+            } else {
+                if (tile) hipLaunchKernelGGL((quant_tile_kernel<XT, false, true>), grid, dim3(kThreads), 0, s, e);
+                else hipLaunchKernelGGL((quant_tile_kernel<XT, false, false>), grid, dim3(kThreads), 0, s, e);
+            }
         }
-    }
     return (int)hipGetLastError();
 }
 

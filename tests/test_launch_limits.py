@@ -20,3 +20,23 @@ def test_router(tmp_path, tokens):
         print(sum(l.grid.x for l in launches()))
     """)
     assert int(out) == -(-tokens // 4)
+
+
+@pytest.mark.parametrize("cols", [(1 << 31) - 128, (1 << 31) - 127, (1 << 31) - 1])
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("tile", [0, 1])
+def test_quantiser_of_long_rows(tmp_path, cols, rows, tile):
+    blocks, row_blocks = -(-cols // 128), -(-rows // 128)
+    out = host_util.run(tmp_path, f"""
+        tile, cols, rows, blocks, row_blocks = {tile}, {cols}, {rows}, {blocks}, {row_blocks}
+        dtype = T.TCM_F16_F32 | (T.TCM_BLOCK_TILE if tile else 0)
+        lds, ldst = (blocks, row_blocks) if tile else (rows, cols)
+        assert T.tcm_quantize_fp8(rows, cols, at(10), cols, dtype, at(11), cols, at(12), lds, at(13), rows, at(14), ldst, None) == T.TCM_OK
+        {CHECK}
+        print(sum(l.grid.x * l.grid.y for l in launches()))
+        hip.stub_clear()
+        assert T.tcm_quantize_fp8(rows, cols, at(10), cols, dtype, at(11), cols, at(12), lds, None, 0, None, 0, None) == T.TCM_OK
+        {CHECK}
+        print(sum(l.grid.x * l.grid.y for l in launches()))
+    """)
+    assert [int(x) for x in out.split()] == [blocks * row_blocks, blocks * (row_blocks if tile else -(-rows // 16))]
