@@ -335,9 +335,10 @@ int moe_impl(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int
     const auto words = [](const void* p) { return ((uintptr_t)p & 3) == 0; };
     const bool tiled = work && topk <= kMoePairs && words(x) && words(w1) && words(w2) && ldx % 2 == 0 && hidden % per_word == 0 &&
                        inter % per_word == 0 && experts * std::max(hidden, inter) < ((int64_t)1 << 26);
-    // (a launch counts its threads in 32 bits: the others take 2^25 waves at most)
+    // (a launch counts its threads in 32 bits: the tiled sum has one an output, the others take 2^25 waves at most)
     const int64_t per_token = std::max<int64_t>(hidden, work ? topk * inter : 0);
-    const int64_t chunk = std::min<int64_t>(tiled ? kMoePairs / topk : ((int64_t)1 << 25) / per_token, tokens);
+    const int64_t most = tiled ? std::min<int64_t>(kMoePairs / topk, (((int64_t)1 << 32) - 256) / hidden) : ((int64_t)1 << 25) / per_token;
+    const int64_t chunk = std::min(most, tokens);
     if (chunk == 0) return TCM_ERR_NOT_SUPPORTED;
     const int64_t h_bytes = (chunk * a.topk * inter * 4 + 15) & ~(int64_t)15, y_bytes = (chunk * a.topk * hidden * 4 + 15) & ~(int64_t)15;
     std::unique_lock<std::mutex> order;

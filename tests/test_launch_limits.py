@@ -40,3 +40,16 @@ def test_quantiser_of_long_rows(tmp_path, cols, rows, tile):
         print(sum(l.grid.x * l.grid.y for l in launches()))
     """)
     assert [int(x) for x in out.split()] == [blocks * row_blocks, blocks * (row_blocks if tile else -(-rows // 16))]
+
+
+@pytest.mark.parametrize("tokens,hidden,inter,experts,topk", [(1024, 1 << 22, 2, 1, 1), (1024, (1 << 26) - 2, 2, 1, 1), (700, 1 << 23, 4, 7, 1),
+                                                              (5000, 1 << 20, 2, 1, 1)])
+def test_expert_layer_of_wide_rows(tmp_path, tokens, hidden, inter, experts, topk):
+    host_util.run(tmp_path, f"""
+        assert T.tcm_moe({tokens}, {hidden}, {inter}, {experts}, {topk}, at(10), {hidden}, at(11), at(12), at(13), None, at(14), None, at(15),
+                         {hidden}, T.TCM_BF16_F32 | T.TCM_C_BF16, None) == T.TCM_OK
+        assert "moe_tile" in T.tcm_last_plan()
+        {CHECK}
+        sums = launches()[2::3]
+        assert sum(l.grid.x for l in sums) * 256 >= {tokens} * {hidden}
+    """)
