@@ -37,9 +37,9 @@ __global__ __launch_bounds__(64 * kWaves) void moe_up_generic(MoeArgs a) {
     const int64_t p = n / a.inter;
     const int i = (int)(n - p * a.inter);
     if (p >= (int64_t)a.tokens * a.topk) return;
-    const int e = a.ids[p];
+    const int64_t e = a.ids[p];
     float g = 0.f, u = 0.f;
-    if ((unsigned)e < (unsigned)a.experts) {
+    if (e >= 0 && e < a.experts) {
         const int64_t mat = (int64_t)a.inter * a.hidden, sm = scale_blocks(a.inter) * scale_blocks(a.hidden);
         const char* wg = (const char*)a.w1 + 2 * e * mat * (W8 ? 1 : 2);
         const char* wu = wg + mat * (W8 ? 1 : 2);
@@ -66,8 +66,8 @@ __global__ __launch_bounds__(64 * kWaves) void moe_down_generic(MoeArgs a) {
     float y = 0.f;
     for (int j = 0; j < a.topk; ++j) {
         const int64_t p = t * a.topk + j;
-        const int e = a.ids[p];
-        if ((unsigned)e >= (unsigned)a.experts) continue;
+        const int64_t e = a.ids[p];
+        if (e < 0 || e >= a.experts) continue;
         const int64_t mat = (int64_t)a.inter * a.hidden, sm = scale_blocks(a.inter) * scale_blocks(a.hidden);
         const char* w = (const char*)a.w2 + e * mat * (W8 ? 1 : 2);
         const float* s = W8 ? a.s2 + e * sm : nullptr;
