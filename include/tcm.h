@@ -509,7 +509,8 @@ const char* tcm_status_string(int status);
  *                  the any-alignment kernel, which also serves what the
  *                  kernel given cannot.
  *   "fp8_split"    0 = planner decides, else the k ranges each of its tiles
- *                  is cut into (1..64, at most one a 128-wide block).
+ *                  is cut into (1..64, at most one a 128-wide block and as
+ *                  many as a launch holds).
  * Unknown keys or out-of-range values: TCM_ERR_INVALID_VALUE.
  * tcm_get_option returns the value, or -2 for an unknown key.
  */

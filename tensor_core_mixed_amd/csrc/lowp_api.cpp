@@ -115,7 +115,9 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         int per_cu;
         double lone, shared, lone_wide, shared_wide;
     } kStep[kNumFp8Tiles] = {{1, 1.28, 1.65, 0, 0}, {1, 0.66, 0.93, 1.6, 1.83}, {2, 0.69, 1.04, 1.2, 2.13}, {2, 0.38, 0.63, 0.75, 1.19}};
-    constexpr int64_t kMaxWgs = (int64_t)1 << 22;  // (a launch counts its threads in 32 bits)
+    // a launch counts its threads in 32 bits: so many workgroups of a product, at most 512 threads each, and of a sum, 256
+    // threads for 1024 outputs
+    constexpr int64_t kMaxWgs = (int64_t)1 << 22, kMaxSums = ((int64_t)1 << 24) - 1;
     constexpr double kFixed = 3.0, kRound = 3.0, kSum = 2.5, kShare = 0.25, kBytesPerUs = 5e6;
     Fp8Plan best{kFp8Generic, 1};
     if (!fp8_tiles_fit(a) || o.fp8_config == kFp8Generic) return best;
@@ -132,10 +134,11 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         const int64_t tiles = ((a.M + t.bm - 1) / t.bm) * ((a.N + t.bn - 1) / t.bn);
         const double lone = wide ? kStep[c].lone_wide : kStep[c].lone, shared = wide ? kStep[c].shared_wide : kStep[c].shared;
         const int64_t slots = 256 * kStep[c].per_cu;
-        for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
-            if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
+        const bool sums = tiles * (t.bm * t.bn / 1024) <= kMaxSums;
+        const int64_t most = std::min({sums ? (int64_t)kFp8MaxSplit : 1, steps, (kMaxWgs - 1) / tiles});
+        for (int s = 1; s <= most; ++s) {
+            if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, most)) continue;
             const int64_t wgs = tiles * s, rest = wgs % slots;
-            if (wgs >= kMaxWgs) break;
             const double step = (double)(wgs / slots) * shared + (rest == 0 ? 0 : lone + (shared - lone) * (double)rest / (double)slots);
             const double rounds = (double)((wgs + slots - 1) / slots);
             const double out = (double)wgs * t.bm * t.bn * (s > 1 ? 4 : c_elem_bytes(a.c_type)) / kBytesPerUs;
@@ -150,9 +153,10 @@ Fp8Plan plan_fp8(const Fp8Args& a, const LowpOpts& o) {
         const int64_t blocks_m = (a.M + kFp8SkinnyRows - 1) / kFp8SkinnyRows;
         const int64_t wgs = blocks_m * ((a.N + kFp8SkinnyCols - 1) / kFp8SkinnyCols);
         const double round = kBlock[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
-        for (int s = 1; s <= std::min<int64_t>(kFp8MaxSplit, steps); ++s) {
-            if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, steps)) continue;
-            if (wgs * s >= kMaxWgs) break;
+        // (1024 outputs a workgroup: the sum's launch holds what this one does)
+        const int64_t most = std::min({(int64_t)kFp8MaxSplit, steps, (kMaxWgs - 1) / wgs});
+        for (int s = 1; s <= most; ++s) {
+            if (o.fp8_split && s != std::min<int64_t>(o.fp8_split, most)) continue;
             const double time = kFixed + std::max((double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round, memory) +
                                 (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t) best_t = time, best = {kFp8Skinny, s};

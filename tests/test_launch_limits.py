@@ -53,3 +53,17 @@ def test_expert_layer_of_wide_rows(tmp_path, tokens, hidden, inter, experts, top
         sums = launches()[2::3]
         assert sum(l.grid.x for l in sums) * 256 >= {tokens} * {hidden}
     """)
+
+
+@pytest.mark.parametrize("config", [-1, 0, 1, 2, 3, 4, 5])
+@pytest.mark.parametrize("split", [0, 2, 64])
+@pytest.mark.parametrize("M,N", [(1 << 17, 1 << 17), ((1 << 18) - 3, 1 << 16), (1 << 12, (1 << 21) - 16), (60, (1 << 27) - 16), (1 << 20, 1 << 16)])
+def test_product_of_many_tiles(tmp_path, config, split, M, N):
+    host_util.run(tmp_path, f"""
+        assert T.tcm_set_option("fp8_config", {config}) == T.tcm_set_option("fp8_split", {split}) == T.TCM_OK
+        st = T.tcm_gemm_fp8({M}, {N}, 8192, at(10), 8192, at(11), {M}, at(12), 8192, at(13), 64, at(14), {N}, T.TCM_E4M3_F32 | T.TCM_C_BF16,
+                            None, 0, None)
+        assert st == T.TCM_OK or st == T.TCM_ERR_NOT_SUPPORTED and not launches(), st
+        if st == T.TCM_OK:
+            {CHECK.strip().replace(chr(10), chr(10) + "    ")}
+    """)
