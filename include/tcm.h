@@ -362,13 +362,16 @@ int tcm_quantize_fp8(int64_t rows, int64_t cols, const void* X, int64_t ldx, int
  * instructions, at twice the rate (the planner's choice; some calls of up to
  * 64 rows get binary32 sums): these add eight products at a time after
  * cutting each to 13 bits below the largest's leading one, and carry those
- * sums in binary32.  On normal data that is off by 2^-16 of C's root mean
- * square on average for any K, 1/32 of f16's own rounding and 1/256 of
+ * sums in binary32.  On normal data that is off by 2^-16 of C's average
+ * size on average for any K, 1/32 of half a step of f16 and 1/256 of
  * bf16's; of the sum of the products' magnitudes by 2^-15 at most from K =
  * 128 on (2^-13 at K = 16), and by 2^-10 in the worst case.  An output that
  * cancels to a small part of its neighbours' size can so be off by more than
  * its own rounding (on normal data one in 50 f16 outputs and one in 400 bf16
- * ones); where that matters, take C in f32.
+ * ones); where that matters, take C in f32.  The product of a block's two
+ * scales is formed first, in binary32: under 2^-126 (the product of the two
+ * blocks' largest values is then under 2^-94) it keeps a subnormal number's
+ * bits, and past the largest binary32 number it is infinite.
  *
  *   M, N, K      sizes, 0 <= size < 2^31; empty and K == 0 as tcm_gemm.
  *   A, lda       M x K, k contiguous, lda >= K; e4m3 or, with TCM_A_E5M2, e5m2.

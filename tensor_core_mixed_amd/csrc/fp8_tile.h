@@ -11,6 +11,9 @@
 // cycles, the multiply-adds the vector ALU for 16; with a scale of its own for
 // every row of B the factor is one more multiplication each, 32).  The MFMA's
 // own block exponents are not used: the scales are arbitrary binary32 values.
+// The two scales are multiplied first, once for sixteen values of a lane: to
+// multiply the sum by one after the other would double the multiply-adds, and
+// differs only where the scales' product leaves binary32's normal range.
 //
 // The MFMA takes its A operand from B's rows and its B operand from A's, so a
 // lane's accumulators run along n at one m: sa is one value a lane and tile,
@@ -83,7 +86,7 @@ __device__ __forceinline__ Operand<WIDE> operand(i8v x) {
     return o;
 }
 // The sum of 128 products.  8-bit operands are taken where C has 16 bits: their instruction cuts products 13 bits below the
-// largest of each eight, off by 2^-16 of C's root mean square on average (1/32 of f16's rounding, 1/256 of bf16's) at
+// largest of each eight, off by 2^-16 of C's average size on average (1/32 of half a step of f16, 1/256 of bf16's) at
 // twice the rate.  Binary32 C takes the 16-bit operands, whose sums are binary32 ones.
 template <bool A5, bool B5, bool WIDE>
 __device__ __forceinline__ f4 mma(const Operand<WIDE>& b, const Operand<WIDE>& a) {

@@ -65,3 +65,26 @@ def test_small_products_next_to_large_ones(options, config):
     check_sums(A, B, E4M3, E4M3, torch.float32, 0)
     B[::2, large] = 448.0
     check_sums(A, B, E4M3, E4M3, torch.bfloat16, 2.0 ** -10)
+
+
+@pytest.mark.parametrize("config", [-1, 0, 1, 2, 3, 4, 5])
+@pytest.mark.parametrize("M", [9, 130])
+@pytest.mark.parametrize("b_row", [False, True])
+def test_scales_whose_product_is_subnormal(options, config, M, b_row):
+    """Such a product is off by half the least step, 2^-150, which a block's sum multiplies."""
+    assert options("fp8_config", config) == T.TCM_OK
+    gen = torch.Generator().manual_seed(M)
+    N, K = 150, 600
+    A, B = (57344 * (2 * torch.rand(M, K, generator=gen) - 1)).to(E5M2).float(), (448 * (2 * torch.rand(N, K, generator=gen) - 1)).to(E4M3).float()
+    power = lambda lo, hi, *s: 2.0 ** torch.randint(lo, hi, s, generator=gen) * (1 + torch.rand(s, generator=gen))
+    sa, sb = power(-90, -74, blocks(K), M), power(-58, -50, *((blocks(K), N) if b_row else (blocks(N), blocks(K))))
+    ref, bound = gemm_ref(A, sa, B, sb, b_row)
+    bound = bound + 2.0 ** -150 * (A.double().abs() @ B.double().abs().t()) + 2.0 ** -149
+    ld = -(-K // 16) * 16
+    Ad, Bd, sad, sbd = padded(A, ld, E5M2).cuda(), padded(B, ld, E4M3).cuda(), sa.cuda(), sb.cuda()
+    C = torch.full((M, N), 7.0, device="cuda")
+    code = T.TCM_E4M3_F32 | T.TCM_A_E5M2 | (T.TCM_B_ROW_SCALES if b_row else 0)
+    assert T.tcm_gemm_fp8(M, N, K, Ad.data_ptr(), ld, sad.data_ptr(), M, Bd.data_ptr(), ld, sbd.data_ptr(), sb.shape[1], C.data_ptr(), N,
+                          code, None, 0, torch.cuda.current_stream().cuda_stream) == T.TCM_OK
+    assert ref.abs().max() > 2.0 ** -120  # (ordinary numbers)
+    check_close(C.cpu(), ref, bound)
