@@ -210,9 +210,11 @@ std::unique_lock<std::mutex> enqueue_order(int dev, void* stream) {
 std::vector<std::pair<int, void*>> g_retired;  // (device, pointer)
 
 // The text of tcm_last_plan: assigned, or (the short calls, which would spend
-// more on it than on their checks) values that are formatted when asked for.
+// more on it than on their checks) values that are formatted when asked for,
+// in place: asking allocates nothing, so it throws nothing.
 struct PlanText {
     std::string s;
+    char formatted[256];
     PlanFormat format = nullptr;
     int64_t v[kPlanValues];
     PlanText& operator=(std::string t) {
@@ -220,13 +222,10 @@ struct PlanText {
         format = nullptr;
         return *this;
     }
-    const std::string& text() {
-        if (format) {
-            char buf[256];
-            format(buf, sizeof buf, v);
-            *this = std::string(buf);
-        }
-        return s;
+    const char* text() {
+        if (!format) return s.c_str();
+        format(formatted, sizeof formatted, v);
+        return formatted;
     }
 };
 thread_local PlanText t_last_plan;
@@ -716,13 +715,14 @@ int tcm_tile_order(int32_t t, int32_t tiles_m, int32_t tiles_n, int32_t* tm, int
 }
 
 int tcm_last_plan(char* buf, int64_t len) {
-    const std::string& s = t_last_plan.text();
+    const char* s = t_last_plan.text();
+    const int64_t size = (int64_t)strlen(s);
     if (buf && len > 0) {
-        int64_t n = std::min<int64_t>(len - 1, (int64_t)s.size());
-        memcpy(buf, s.data(), (size_t)n);
+        int64_t n = std::min<int64_t>(len - 1, size);
+        memcpy(buf, s, (size_t)n);
         buf[n] = 0;
     }
-    return (int)s.size();
+    return (int)size;
 }
 
 void tcm_release_workspace(void) {
@@ -1361,7 +1361,7 @@ int tcm_tune(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
     const int cs = c_elem_bytes(p.c_type);
     p.aligned = ((uintptr_t)A % 16 == 0) && ((uintptr_t)B % 16 == 0) && ((uintptr_t)C % 16 == 0) &&
                 (!use_bias || (uintptr_t)bias % 16 == 0) && ((uintptr_t)C % cs == 0);
-    if (strstr(t_last_plan.text().c_str(), "kernel=generic")) return TCM_OK;  // the generic kernel: nothing to choose
+    if (strstr(t_last_plan.text(), "kernel=generic")) return TCM_OK;  // the generic kernel: nothing to choose
     hipStream_t s = (hipStream_t)stream;
     hipEvent_t e0, e1;
     if (hipEventCreate(&e0) != hipSuccess) return TCM_ERR_HIP;
