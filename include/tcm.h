@@ -391,8 +391,11 @@ int tcm_quantize_fp8(int64_t rows, int64_t cols, const void* X, int64_t ldx, int
  * a gradient).  Any alignment and leading dimension is served; the fast
  * kernels take A, B and C 16-byte aligned with lda and ldb multiples of 16.
  * SA, SB and bias are 4-byte aligned.  K needs no alignment: bytes between K
- * and the leading dimension are never used.
- * Returns as tcm_gemm; the workspace rules are tcm_gemm's.
+ * and the leading dimension are never used (the fast kernels read them as far
+ * as the aligned 16 bytes that a row's last ones lie in, in the last row too).
+ * Returns as tcm_gemm, and TCM_ERR_NOT_SUPPORTED where the any-alignment
+ * kernel's 64 x 64 tiles would be 2^24 or more; the workspace rules are
+ * tcm_gemm's.
  */
 int tcm_gemm_fp8(int64_t M, int64_t N, int64_t K,
                  const void* A, int64_t lda, const float* SA, int64_t ldsa,
@@ -449,8 +452,12 @@ int tcm_moe_route(int64_t tokens, int64_t experts, int64_t topk,
  *                optionally | TCM_W_E4M3.
  * Sums are binary32; the products between the two matrices stay in binary32
  * or in two 16-bit parts that hold it to 16 bits or more.  Any alignment of
- * X, W1, W2 and out; ids, weights and scales 4-byte aligned.  Returns as
- * tcm_gemm; the workspace rules are tcm_gemm's.
+ * X, W1, W2 and out; ids, weights and scales 4-byte aligned.  An expert's
+ * weights are read once for every 32 of its pairs (16 up to 16 tokens), and a
+ * call of more than 1024 pairs is cut into parts that read them anew: a prompt
+ * is served, but not at the rate of its products.  Returns as tcm_gemm, and
+ * TCM_ERR_NOT_SUPPORTED where the any-alignment kernels would take more than
+ * 2^25 values of a token; the workspace rules are tcm_gemm's.
  */
 int tcm_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t topk,
             const void* X, int64_t ldx, const int32_t* ids, const float* weights,

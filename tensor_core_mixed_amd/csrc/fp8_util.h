@@ -8,8 +8,6 @@
 
 namespace tcm {
 
-typedef float f2_t __attribute__((ext_vector_type(2)));
-
 template <bool E5M2>
 __device__ __forceinline__ float fp8_decode(unsigned byte) {
     if constexpr (E5M2) return __builtin_amdgcn_cvt_f32_bf8((int)byte, 0);

@@ -5,19 +5,25 @@
 //     y[p][c]   = W2[e] row c . h[p],
 //     out[t][c] = sum over t's slots of y, in slot order.
 //
-// The chosen experts' weights bind the time, and each is read once: a
-// workgroup takes one expert and a block of its rows (16 of gate and up, 64
-// of W2) and multiplies them with all pairs of that expert, 16 or 32
-// at a time, on 16x16x32 MFMAs with the weights' rows as one operand and the
-// pairs as the other.  Weights go straight from memory to registers; the
-// waves deal k among themselves, the loads of the next steps in flight, and
-// add their sums in LDS in wave order.  Every workgroup finds its pairs itself
-// by one pass over the ids.  24 bf16 tokens, four of 32 experts of
-// 4096 x 1536 each, take 216 us, 5.4 TB/s, bound by memory; one token of eight
-// 8-bit experts of 2048 x 1024 18 us, of which 10 are its bytes.  Three
-// launches: up, down, sum over the slots.  (The
-// sum left to the last workgroup of 64 columns took one token of eight experts
-// from 17.9 to 17.3 us and four tokens from 47.5 to 48.6.)
+// The chosen experts' weights bind the time.  A workgroup takes one expert
+// and a block of its rows (16 of gate and up, 64 of W2) and multiplies them
+// with all pairs of that expert, 16 (calls of up to 16 tokens) or 32 at a
+// time, on 16x16x32 MFMAs with the weights' rows as one operand and the
+// pairs as the other: weights are read once for every 16 or 32 pairs of their
+// expert, and again in each part of kMoePairs pairs that a longer call is cut
+// into.  They go straight from memory to registers; the waves deal k among
+// themselves, the loads of the next steps in flight, and add their sums in LDS
+// in wave order.  Every workgroup finds its pairs itself by one pass over the
+// ids.  Three launches: up, down, sum over the slots.  (The sum left to the
+// last workgroup of 64 columns took one token of eight experts from 17.9 to
+// 17.3 us and four tokens from 47.5 to 48.6.)
+//
+// 24 bf16 tokens, four of 32 experts of 4096 x 1536 each, take 211 to 217 us,
+// 5.4 TB/s, bound by memory, and in 8 bits 154 (3.7 TB/s: a step of an 8-bit
+// row is half a line, and another wave reads the other half); one token of
+// eight 8-bit experts of 2048 x 1024 18 us, of which 8 are its bytes.  2048
+// tokens take 3.4 ms in bf16 and 2.7 in 8 bits (92 and 115 TFLOP/s): eight
+// parts, each of which reads every expert once or twice.
 //
 // 8-bit weights are taken to 16-bit floats (exactly) and a 128-wide block's
 // sums scaled by its tile's scale.  h goes to the matrix cores as the
@@ -302,7 +308,8 @@ __device__ __forceinline__ void split8(const i4 (&v)[2], float f, i4& hi, i4& lo
     }
 }
 
-// Row tiles of W2 a workgroup (with two, 8% slower).
+// Row tiles of W2 a workgroup (with two, 24 bf16 tokens of the layer above 217.0 us and 216.7 with four; one token of eight
+// 8-bit experts 18.2 and 18.9).
 constexpr int kDownTiles = 4, kDownRows = 16 * kDownTiles;
 
 // A step is 32 k (8-bit weights: 64 k): 16 bytes of a row a lane.
