@@ -83,14 +83,6 @@ def check_close(got, ref, bound):
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off; worst {((got - ref).abs() / bound.clamp_min(1e-300)).max():.3f} of the bound"
 
 
-def eight_bits(gen, rows, cols, t, ld=None, spread_rows=True):
-    """A quantised matrix with rows at leading dimension ld, its bytes past cols all NaN codes, and its row-block scales."""
-    x = torch.randn(rows, cols, generator=gen)
-    if spread_rows:
-        x = x * torch.exp(torch.randn(rows, 1, generator=gen))
-    return x
-
-
 def padded(q, ld, t):
     """q (rows, cols) in type t inside a (rows, ld) buffer whose other bytes are NaN codes."""
     rows, cols = q.shape
