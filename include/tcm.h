@@ -29,16 +29,17 @@
  * process-wide switches and tuning table below (mutex-protected).  Host
  * threads may call on one stream at once: launches that hand results on
  * through its workspace are enqueued with no other call's use of it between
- * them.  The workspace grows on demand (hipMalloc, plus a zero-fill kernel
- * for its counters), never synchronising; an outgrown buffer is kept, not freed,
- * until tcm_release_workspace, because kernels or graphs enqueued earlier may
- * still use it.  A call whose plan fits the stream's existing workspace
- * allocates nothing and issues only kernel launches, so it can be captured
- * into a HIP graph after one warm-up call of the same shape on that stream; a
- * call that would grow the workspace while its stream is capturing returns
- * TCM_ERR_NOT_SUPPORTED.  A captured graph uses the workspace of the stream
- * it was captured on: its replays must not run at the same time as other
- * calls (eager or replayed) on that stream's workspace, e.g. replay it on the
+ * them (hipStreamPerThread has a workspace for every thread).  The workspace
+ * grows on demand (hipMalloc, plus a zero-fill kernel for its counters), never
+ * synchronising; an outgrown buffer is kept, not freed, until
+ * tcm_release_workspace, because kernels or graphs enqueued earlier may still
+ * use it.  A call whose plan fits the stream's existing workspace allocates
+ * nothing and issues only kernel launches, so it can be captured into a HIP
+ * graph after one warm-up call of the same shape on that stream; a call that
+ * would grow the workspace while its stream is capturing returns
+ * TCM_ERR_NOT_SUPPORTED.  A captured graph uses the workspace of the stream it
+ * was captured on: its replays must not run at the same time as other calls
+ * (eager or replayed) on that stream's workspace, e.g. replay it on the
  * same stream.  tcm_gemm_noalloc needs no workspace at all.
  *
  * Errors are returned, never raised; argument checks run before any HIP call.

@@ -5,6 +5,7 @@
 #include <dlfcn.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -188,18 +189,27 @@ struct Workspace {
     int* counters = nullptr;
     int64_t n_counters = 0;
 };
-std::map<std::pair<int, void*>, Workspace> g_ws;  // (device, stream) -> workspace
+std::map<std::pair<int, void*>, Workspace> g_ws;  // (device, stream_key) -> workspace
+// The stream's handle; but hipStreamPerThread is one handle for a stream of
+// every thread, so there a number of the thread's own (odd, as no other
+// handle but hipStreamLegacy's 1 is).
+void* stream_key(void* stream) {
+    if (stream != (void*)hipStreamPerThread) return stream;
+    static std::atomic<uintptr_t> next{3};
+    thread_local const uintptr_t mine = next.fetch_add(2);
+    return (void*)mine;
+}
 // Held from the look-up of a stream's workspace (or of the fixed scratch) to
 // the last launch of the call: a call of several launches hands its partial
 // results on through it, so another host thread's launches on the same stream
 // must not come between them.  Streams have locks of their own: one stream's
 // full queue holds no other up.  (Taken before g_mu, never after it.)
-std::map<std::pair<int, void*>, std::mutex> g_enqueue;  // (device, stream) -> lock
+std::map<std::pair<int, void*>, std::mutex> g_enqueue;  // (device, stream_key) -> lock
 std::unique_lock<std::mutex> enqueue_order(int dev, void* stream) {
     std::mutex* m;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        m = &g_enqueue[{dev, stream}];
+        m = &g_enqueue[{dev, stream_key(stream)}];
     }
     return std::unique_lock<std::mutex>(*m);
 }
@@ -427,7 +437,7 @@ int64_t round_pow2(int64_t x) {
 }
 int get_workspace(int dev, void* stream, int64_t partial_bytes, int64_t n_counters, Workspace* out) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace& w = g_ws[{dev, stream}];
+    Workspace& w = g_ws[{dev, stream_key(stream)}];
     const bool grow_p = w.partial_bytes < partial_bytes, grow_c = w.n_counters < n_counters;
     if (grow_p || grow_c) {
         hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;

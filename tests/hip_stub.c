@@ -16,7 +16,7 @@ typedef struct {
 
 enum { MAX = 1 << 16 };
 static launch_t launches[MAX];
-static int count, pause_us;
+static int count, mallocs, pause_us;
 static uint64_t next_address = (uint64_t)1 << 45;
 static pthread_mutex_t mu = PTHREAD_MUTEX_INITIALIZER;
 static __thread struct {
@@ -27,6 +27,7 @@ static __thread struct {
 
 /* the test's side */
 int stub_count(void) { return count; }
+int stub_mallocs(void) { return mallocs; }
 void stub_clear(void) { count = 0; }
 void stub_pause(int us) { pause_us = us; } /* after each launch */
 const launch_t* stub_launches(void) { return launches; }
@@ -58,6 +59,7 @@ int hipMalloc(void** p, size_t n) {
     pthread_mutex_lock(&mu);
     *p = (void*)next_address;
     next_address += (n + 4095) & ~(size_t)4095;
+    ++mallocs;
     pthread_mutex_unlock(&mu);
     return 0;
 }

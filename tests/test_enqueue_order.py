@@ -59,3 +59,23 @@ def test_launches_of_a_call_stay_together(tmp_path, name):
         for i in range(0, len(who), per_call):
             assert len(set(who[i:i + per_call])) == 1, (i, [sorted(set(who)).index(w) for w in who])
     """)
+
+
+def test_each_threads_own_default_stream_has_a_workspace_of_its_own(tmp_path):
+    """One handle, hipStreamPerThread, names another stream in every thread: their work may overlap."""
+    host_util.run(tmp_path, """
+        per_thread = 2  # (the handle's value)
+        def call(p=lambda i: at(10 + i)):
+            return T.tcm_moe(4, 256, 128, 8, 2, p(0), 256, p(1), p(2), p(3), None, p(4), None, p(5), 256, T.TCM_BF16_F32 | T.TCM_C_BF16,
+                             per_thread)
+        assert call() == call() == T.TCM_OK and hip.stub_mallocs() == 1
+        done, go = [], threading.Barrier(2)
+        def run():
+            done.append(call() == call() == T.TCM_OK)
+            go.wait()  # (both threads live at once)
+        ts = [threading.Thread(target=run) for _ in range(2)]
+        [t.start() for t in ts]
+        [t.join() for t in ts]
+        assert done == [True, True] and hip.stub_mallocs() == 3, hip.stub_mallocs()
+        assert call() == T.TCM_OK and hip.stub_mallocs() == 3
+    """)

@@ -47,7 +47,14 @@ def few_rows_caller(seed, stream):
 
 
 def test_threads_on_one_stream():
-    s = torch.cuda.current_stream().cuda_stream
+    check_threads(torch.cuda.current_stream().cuda_stream)
+
+
+def test_threads_on_their_own_default_streams():
+    check_threads(2)  # (hipStreamPerThread, one handle for a stream of each thread)
+
+
+def check_threads(s):
     callers = [moe_caller(0, s), moe_caller(1, s), product_caller(2, s, 300), product_caller(3, s, 40), few_rows_caller(4, s)]
     alone = []
     for call, new in callers:
