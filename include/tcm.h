@@ -95,6 +95,11 @@ enum { TCM_F16_F32 = 0, TCM_BF16_F32 = 1, TCM_F32_F32 = 2, TCM_I8_I32 = 3 };
  *                  the two flags e5m2 (largest 57344), with binary32 scales;
  *                  accumulate and C in binary32; bias f32                   */
 enum { TCM_E4M3_F32 = 4 };
+/*   TCM_MXFP4_F32 : tcm_gemm_mxfp4's element type: A and B 4-bit floats, e2m1
+ *                   (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), with a
+ *                   power of two for each block of 32; accumulate and C in
+ *                   binary32; bias f32                                     */
+enum { TCM_MXFP4_F32 = 5 };
 /* flags of tcm_gemm_fp8 */
 #define TCM_A_E5M2 (1 << 12)
 #define TCM_B_E5M2 (1 << 13)
@@ -464,6 +469,149 @@ int tcm_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int6
             const void* X, int64_t ldx, const int32_t* ids, const float* weights,
             const void* W1, const float* S1, const void* W2, const float* S2,
             void* out, int64_t ldo, int dtype, void* stream);
+
+/*
+ * tcm_quantize_mxfp4 -- a matrix to 4-bit floats with a power of two for each
+ * block of 32 of its values (the microscaled format MXFP4: e2m1 values under
+ * e8m0 scales; the mixed precision of the Tensor Core notes,
+ * je-d.tistory.com/entry/tvm, narrower still):
+ *
+ *     e = clamp(floor(log2 amax |x|) - 2, -127, 127),
+ *     q = nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives to x / 2^e,
+ *         ties to the even code; what lies above 6 becomes 6.
+ *
+ * X, rows, cols, ldx and dtype as tcm_quantize_fp8 (no flags).  Two outputs,
+ * either of which may be NULL (not both), from one read of X:
+ *
+ *   Q, S     X as it lies, blocks of 32 consecutive columns.  Two values a
+ *            byte, the even column's in the lower half: Q[r*ldq + c/2], ldq
+ *            (BYTES) >= ceil(cols/2).  Scales are bytes e + 127, four
+ *            consecutive blocks' in one 32-bit word, the first lowest:
+ *            (S[(c/128)*lds + r] >> 8*(c/32 % 4)) & 255, lds >= rows.
+ *   QT, ST   X transposed, blocks of 32 consecutive rows: QT[c*ldqt + r/2],
+ *            ST[(r/128)*ldst + c], ldqt >= ceil(rows/2), ldst >= cols.
+ *
+ * (Q, S) and (QT, ST) are operands of tcm_gemm_mxfp4 as they come.  (Scales
+ * stored a byte a block, [row][block], become words by viewing four bytes as
+ * one and transposing.)  The half byte past an odd row's end and the scale
+ * bytes of blocks past it are zeros; bytes further on are not written.  A
+ * block that holds a NaN or an infinity has the scale NaN (255) and zeros.
+ * Any alignment and leading dimension of X, Q and QT; S and ST 4-byte
+ * aligned.  Outputs must not overlap X or each other.  rows or cols 0:
+ * nothing to do.  Returns TCM_OK once enqueued; TCM_ERR_INVALID_VALUE;
+ * TCM_ERR_HIP.  Allocates nothing.
+ */
+int tcm_quantize_mxfp4(int64_t rows, int64_t cols, const void* X, int64_t ldx, int dtype,
+                       void* Q, int64_t ldq, uint32_t* S, int64_t lds,
+                       void* QT, int64_t ldqt, uint32_t* ST, int64_t ldst, void* stream);
+
+/*
+ * tcm_dequantize_mxfp4 -- the values q 2^e that (Q, S) stand for, rounded to
+ * X's type (exact in f32 and bf16 from 2^-126 to their largest, in f16 from
+ * 2^-14): 4-bit weights for a product in 16 bits, or what a rounding to 4
+ * bits left of X.  Arguments as tcm_quantize_mxfp4; X is written and must not
+ * overlap Q or S.  Under a NaN scale every value is NaN.  Allocates nothing.
+ */
+int tcm_dequantize_mxfp4(int64_t rows, int64_t cols, const void* Q, int64_t ldq,
+                         const uint32_t* S, int64_t lds, void* X, int64_t ldx, int dtype,
+                         void* stream);
+
+/*
+ * tcm_gemm_mxfp4 -- the product of two matrices in 4-bit floating point with
+ * a power of two for each block of 32 along k,
+ *
+ *     C[m][n] = epi( [C_in[m][n] +] bias[n] + sum over blocks b of
+ *                    2^(ea[b, m] + eb[b, n]) * sum_{k in block b} A[m][k] * B[n][k] ).
+ *
+ * A block's products are summed exactly (they are multiples of 1/4 below
+ * 2^11); scaled blocks are added in binary32.
+ *
+ *   M, N, K      sizes, 0 <= size < 2^31; empty and K == 0 as tcm_gemm.
+ *   A, lda       M x K as tcm_quantize_mxfp4 writes it; lda (BYTES) >= ceil(K/2).
+ *   SA, ldsa     A's scale words, [ceil(K/128)][ldsa], ldsa >= M.
+ *   B, ldb       N x K, ldb (BYTES) >= ceil(K/2).
+ *   SB, ldsb     B's scale words, [ceil(K/128)][ldsb], ldsb >= N.
+ *   C, ldc       M x N row-major, ldc >= N; f32, or by TCM_C_F16 / TCM_C_BF16
+ *                rounded to nearest even.  Must not overlap an input.
+ *   dtype        TCM_MXFP4_F32, optionally with an output type flag.
+ *   bias, epilogue, stream   as tcm_gemm (all of TCM_EPI_*; bias is float).
+ *
+ * A training step's three products are this one, as tcm_gemm_fp8's.  A scale
+ * byte of 255 is NaN, and so is every output of its row (of its column, for
+ * B's).  Any alignment and leading dimension is served; the fast kernels take
+ * A, B and C 16-byte aligned with lda and ldb multiples of 16.  SA, SB and
+ * bias are 4-byte aligned.  K needs no alignment: values and scale bytes
+ * between K and a row's or a word's end are never used (the fast kernels read
+ * them as far as the aligned 16 bytes that a row's last ones lie in, in the
+ * last row too).  Returns as tcm_gemm, and TCM_ERR_NOT_SUPPORTED where the
+ * any-alignment kernel's 64 x 64 tiles would be 2^24 or more; the workspace
+ * rules are tcm_gemm's.
+ */
+int tcm_gemm_mxfp4(int64_t M, int64_t N, int64_t K,
+                   const void* A, int64_t lda, const uint32_t* SA, int64_t ldsa,
+                   const void* B, int64_t ldb, const uint32_t* SB, int64_t ldsb,
+                   void* C, int64_t ldc, int dtype, const float* bias, int epilogue,
+                   void* stream);
+
+/*
+ * tcm_moe_balance -- what a router's training watches: how often each expert
+ * is chosen, the loss that balances the experts' load, and the loss that
+ * keeps the logits small,
+ *
+ *     p         = softmax(x) over the experts, or with TCM_ROUTE_SIGMOID
+ *                 s / (sum over the experts of s), s = 1 / (1 + exp(-x)),
+ *     counts[e] = the slots of ids that hold e,  counts[experts] = T, the tokens that count,
+ *     losses[0] = experts * sum_e counts[e] / (T * topk) * mean over tokens of p_e,
+ *     losses[1] = mean over tokens of log(sum_e exp(x_e))^2.
+ *
+ *   logits, ldx  tokens x experts, ldx >= experts, of the type in `dtype`
+ *                (TCM_F16_F32, TCM_BF16_F32 or TCM_F32_F32; any alignment).
+ *   ids          tokens x topk, dense (tcm_moe_route's); an id outside
+ *                [0, experts) is counted nowhere, one that repeats each time.
+ *   mask         tokens bytes, or NULL: a token whose byte is 0 (padding)
+ *                counts nowhere, whatever its logits hold.
+ *   counts       experts + 1 integers;  losses: 2 floats.  Written whole, zeros
+ *                where no token counts.  Must not overlap an input.
+ * Weigh losses[0] and losses[1] as the training does; their gradient is
+ * tcm_moe_route_grad's.  experts <= 1024, topk <= 64 and tokens * topk < 2^31
+ * (else TCM_ERR_NOT_SUPPORTED), topk <= experts, tokens < 2^31.  A token whose
+ * logits are all -inf adds nothing to the losses; NaN and +inf logits make
+ * them NaN.  The same call gives the same bits.  Returns as tcm_gemm; the
+ * workspace rules are tcm_gemm's (calls of up to 128 tokens use none).
+ */
+int tcm_moe_balance(int64_t tokens, int64_t experts, int64_t topk,
+                    const void* logits, int64_t ldx, int dtype,
+                    const int32_t* ids, const uint8_t* mask,
+                    int32_t* counts, float* losses, void* stream);
+
+/*
+ * tcm_moe_route_grad -- the gradient of a router by its logits: of the
+ * weights that tcm_moe_route gave the ids (the choice itself is held fixed)
+ * and of tcm_moe_balance's two losses (the counts are held fixed),
+ *
+ *     D[t] = sum over slots j of dweights[t][j] * d weight[t][j] / d x[t]
+ *            + dlosses[0] * d losses[0] / d x[t] + dlosses[1] * d losses[1] / d x[t].
+ *
+ *   logits, ldx, ids, mask   as tcm_moe_balance.  A masked token's row is zeros.
+ *   dtype        tcm_moe_route's: the logits' type, TCM_ROUTE_SIGMOID,
+ *                TCM_ROUTE_NORM; and TCM_C_F16 or TCM_C_BF16 for D's type (f32).
+ *   scale        tcm_moe_route's.
+ *   dweights     tokens x topk floats, or NULL: no gradient of the weights.
+ *                (A slot whose id lies outside [0, experts) has no weight.)
+ *   counts       tcm_moe_balance's experts + 1 integers, or their sums over
+ *                the ranks that share a batch; read with dlosses only.
+ *   dlosses      2 floats in device memory, or NULL: no gradient of the losses.
+ *   D, ldd       tokens x experts, ldd >= experts; written; any alignment.  Must
+ *                not overlap an input.
+ * (tcm_moe_route's bias moves the choice only, so it plays no part.)  A token
+ * whose logits are all -inf has a row of zeros; NaN and +inf logits give NaN.
+ * Limits and statuses as tcm_moe_balance.  Allocates nothing.
+ */
+int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
+                       const void* logits, int64_t ldx, int dtype, float scale,
+                       const int32_t* ids, const uint8_t* mask, const float* dweights,
+                       const int32_t* counts, const float* dlosses,
+                       void* D, int64_t ldd, void* stream);
 
 /* Text of a status code (static storage; never NULL). */
 const char* tcm_status_string(int status);

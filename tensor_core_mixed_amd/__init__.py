@@ -20,6 +20,7 @@ TCM_F16_F32, TCM_BF16_F32, TCM_F32_F32, TCM_I8_I32 = 0, 1, 2, 3
 TCM_A_COLMAJOR, TCM_B_COLMAJOR = 1 << 8, 1 << 9
 TCM_C_F16, TCM_C_BF16 = 1 << 10, 1 << 11
 TCM_E4M3_F32 = 4
+TCM_MXFP4_F32 = 5
 TCM_A_E5M2, TCM_B_E5M2, TCM_B_ROW_SCALES = 1 << 12, 1 << 13, 1 << 14
 TCM_Q_E5M2, TCM_BLOCK_TILE = 1 << 15, 1 << 16
 TCM_ROUTE_SIGMOID, TCM_ROUTE_NORM = 1 << 17, 1 << 18
@@ -82,6 +83,16 @@ def lib():
         L.tcm_moe_route.restype = ci
         L.tcm_moe.argtypes = [i64] * 5 + [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci, vp]
         L.tcm_moe.restype = ci
+        L.tcm_quantize_mxfp4.argtypes = [i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.tcm_quantize_mxfp4.restype = ci
+        L.tcm_dequantize_mxfp4.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, ci, vp]
+        L.tcm_dequantize_mxfp4.restype = ci
+        L.tcm_gemm_mxfp4.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, ci, vp]
+        L.tcm_gemm_mxfp4.restype = ci
+        L.tcm_moe_balance.argtypes = [i64, i64, i64, vp, i64, ci, vp, vp, vp, vp, vp]
+        L.tcm_moe_balance.restype = ci
+        L.tcm_moe_route_grad.argtypes = [i64, i64, i64, vp, i64, ci, ctypes.c_float, vp, vp, vp, vp, vp, vp, i64, vp]
+        L.tcm_moe_route_grad.restype = ci
         L.tcm_status_string.argtypes = [ci]
         L.tcm_status_string.restype = ctypes.c_char_p
         L.tcm_set_option.argtypes = [ctypes.c_char_p, i64]
@@ -273,6 +284,36 @@ def tcm_moe(tokens, hidden, inter, experts, topk, X, ldx, ids, weights, W1, S1, 
     """A mixture-of-experts layer for a few tokens.  Returns the tcm status
     code."""
     return lib().tcm_moe(tokens, hidden, inter, experts, topk, X, ldx, ids, weights, W1, S1, W2, S2, out, ldo, dtype, stream)
+
+
+def tcm_quantize_mxfp4(rows, cols, X, ldx, dtype, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream):
+    """X in 4-bit floats with a power of two a block of 32, as it lies (Q, S)
+    and/or transposed (QT, ST).  Returns the tcm status code."""
+    return lib().tcm_quantize_mxfp4(rows, cols, X, ldx, dtype, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream)
+
+
+def tcm_dequantize_mxfp4(rows, cols, Q, ldq, S, lds, X, ldx, dtype, stream):
+    """The values that (Q, S) stand for.  Returns the tcm status code."""
+    return lib().tcm_dequantize_mxfp4(rows, cols, Q, ldq, S, lds, X, ldx, dtype, stream)
+
+
+def tcm_gemm_mxfp4(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, dtype, bias, epilogue, stream):
+    """C = epi(bias + A.B^T) of 4-bit operands with block scales.  Returns
+    the tcm status code."""
+    return lib().tcm_gemm_mxfp4(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, dtype, bias, epilogue, stream)
+
+
+def tcm_moe_balance(tokens, experts, topk, logits, ldx, dtype, ids, mask, counts, losses, stream):
+    """How often each expert is chosen, and the router's losses.  Returns the
+    tcm status code."""
+    return lib().tcm_moe_balance(tokens, experts, topk, logits, ldx, dtype, ids, mask, counts, losses, stream)
+
+
+def tcm_moe_route_grad(tokens, experts, topk, logits, ldx, dtype, scale, ids, mask, dweights, counts, dlosses, D, ldd, stream):
+    """The gradient of a router's weights and losses by its logits.  Returns
+    the tcm status code."""
+    return lib().tcm_moe_route_grad(tokens, experts, topk, logits, ldx, dtype, scale, ids, mask, dweights, counts, dlosses, D, ldd,
+                                    stream)
 
 
 def tcm_version():

@@ -82,8 +82,90 @@ __device__ __forceinline__ void store_c_any(char* p, int c_type, float v) {
     }
 }
 
+typedef float c4_t __attribute__((ext_vector_type(4)));
+// E consecutive columns n .. of rows of C
+template <int E, class Args>
+struct Epilogue {
+    const Args& a;
+    int64_t n;
+    bool full;  // all of them exist
+    float bias[E];
+
+    __device__ __forceinline__ Epilogue(const Args& a, int64_t n) : a(a), n(n), full(n + E <= a.N) {
+        if (a.has_bias) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) bias[j] = a.bias[min(n + j, a.N - 1)];
+        }
+    }
+    // v += row m of C
+    __device__ __forceinline__ void add_c(float (&v)[E], const char* c) const {
+        if (full && a.c_vec) {
+            if (a.c_type == C_ACC) {
+#pragma unroll
+                for (int q = 0; q < E / 4; ++q) {
+                    const c4_t x = *(const c4_t*)(c + 16 * q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[4 * q + i] += x[i];
+                }
+            } else {
+                unsigned w[E / 2];
+                __builtin_memcpy(w, __builtin_assume_aligned(c, E >= 8 ? 16 : 8), 2 * E);
+#pragma unroll
+                for (int q = 0; q < E; ++q) {
+                    const unsigned short h = (unsigned short)(w[q >> 1] >> (16 * (q & 1)));
+                    v[q] += a.c_type == C_F16 ? (float)__builtin_bit_cast(_Float16, h) : __builtin_bit_cast(float, (unsigned)h << 16);
+                }
+            }
+        } else {
+            const int cs = c_elem_bytes(a.c_type);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += load_c_any(c + min<int64_t>(j, a.N - 1 - n) * cs, a.c_type);
+        }
+    }
+    // v + bias + C's contents, ReLU, stored in C's type as row m
+    __device__ __forceinline__ void store(float (&v)[E], int64_t m) const {
+        char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
+        if (a.has_bias) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += bias[j];
+        }
+        if (a.accum) add_c(v, c);
+        if (a.relu) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = v[j] > 0.f ? v[j] : 0.f;
+        }
+        if (full && a.c_vec) {
+            if (a.c_type == C_ACC) {
+#pragma unroll
+                for (int q = 0; q < E / 4; ++q) *(c4_t*)(c + 16 * q) = c4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            } else {
+                unsigned w[E / 2];
+#pragma unroll
+                for (int q = 0; q < E / 2; ++q) {
+                    unsigned lo, hi;
+                    if (a.c_type == C_F16) {
+                        lo = __builtin_bit_cast(unsigned short, (_Float16)v[2 * q]);
+                        hi = __builtin_bit_cast(unsigned short, (_Float16)v[2 * q + 1]);
+                    } else {
+                        lo = __builtin_bit_cast(unsigned short, (__bf16)v[2 * q]);
+                        hi = __builtin_bit_cast(unsigned short, (__bf16)v[2 * q + 1]);
+                    }
+                    w[q] = lo | hi << 16;
+                }
+                __builtin_memcpy(__builtin_assume_aligned(c, E >= 8 ? 16 : 8), w, 2 * E);
+            }
+        } else {
+            const int cs = c_elem_bytes(a.c_type);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (n + j < a.N) store_c_any(c + j * cs, a.c_type, v[j]);
+        }
+    }
+};
+
 // one element of C from its sum: + bias, + C's contents, ReLU, rounded to C's type
-__device__ __forceinline__ void store_epilogue(const Fp8Args& a, float v, int64_t m, int64_t n) {
+template <class Args>
+__device__ __forceinline__ void store_epilogue(const Args& a, float v, int64_t m, int64_t n) {
     if (a.has_bias) v += load_float<F32>((const char*)a.bias, n);
     char* c = (char*)a.C + (m * a.ldc + n) * c_elem_bytes(a.c_type);
     if (a.accum) v += load_c_any(c, a.c_type);

@@ -88,6 +88,43 @@ struct RouteArgs {
 constexpr int kRouteMaxExperts = 1024, kRouteMaxTopk = 64;
 int launch_route(int x_type, const RouteArgs& a, void* stream);
 
+struct BalanceArgs {
+    const void* x;         // [tokens][experts]
+    int64_t tokens, ldx;
+    int experts, topk;
+    int sigmoid;
+    const int* ids;        // [tokens][topk]
+    const unsigned char* mask;  // [tokens], 0: the token does not count; or null
+    int* counts;           // [experts + 1], the last the tokens that count
+    float* losses;         // [2]
+    // several workgroups: each one's partial sums, and what the second launch's hand on
+    int groups;
+    float* p;              // [groups][experts]
+    int* n;                // [groups][experts + 1]
+    double* z;             // [groups]
+    double* share;         // [experts / 64]
+    int* arrived;
+};
+// a workgroup's waves in the two ways to run, and the most workgroups of the second
+constexpr int kBalanceWaves = 8, kBalanceOneWaves = 16, kBalanceGroups = 256, kBalanceOneTokens = 128;
+int launch_balance(int x_type, const BalanceArgs& a, void* stream);
+
+struct RouteGradArgs {
+    const void* x;
+    int64_t tokens, ldx;
+    int experts, topk;
+    int sigmoid, norm, d_type;
+    float scale;
+    const int* ids;
+    const unsigned char* mask;
+    const float* dweights; // [tokens][topk] or null
+    const int* counts;     // BalanceArgs::counts, with dlosses
+    const float* dlosses;  // [2] or null
+    void* d;               // [tokens][experts]
+    int64_t ldd;
+};
+int launch_route_grad(int x_type, const RouteGradArgs& a, void* stream);
+
 struct MoeArgs {
     const void* x;         // [tokens][hidden], 16-bit
     int64_t ldx;
@@ -111,6 +148,49 @@ struct MoeArgs {
 constexpr int kMoePairs = 1024;
 int launch_moe_tile(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
 int launch_moe_generic(int x_type, bool w_e4m3, const MoeArgs& a, void* stream);
+
+// ---- 4-bit floats (e2m1) with a power of two for each block of 32 (MXFP4)
+
+// Four scales of a row's consecutive blocks lie in one word, the first lowest.
+constexpr int kMxBlock = 32, kMxWord = 4 * kMxBlock;
+constexpr int64_t mx_words(int64_t n) { return (n + kMxWord - 1) / kMxWord; }
+constexpr int64_t mx_bytes(int64_t n) { return (n + 1) / 2; }
+
+struct MxQuantArgs {
+    const void* x;
+    int64_t rows, cols, ldx;
+    unsigned char* q;      // [rows][cols / 2] as x lies, or null
+    int64_t ldq;           // bytes
+    unsigned* s;           // [cols / 128][rows]
+    int64_t lds;
+    unsigned char* qt;     // [cols][rows / 2], or null
+    int64_t ldqt;
+    unsigned* st;          // [rows / 128][cols]
+    int64_t ldst;
+};
+// x_type: F16, BF16 or F32
+int launch_mx_quantize(int x_type, const MxQuantArgs& a, void* stream);
+// x from (q, s)
+int launch_mx_dequantize(int x_type, const MxQuantArgs& a, void* stream);
+
+struct Fp4Args {
+    const unsigned char* A;  // [M][K / 2]
+    const unsigned char* B;  // [N][K / 2]
+    void* C;                 // [M][N]
+    const unsigned* sa;      // [k / 128][row of A]
+    const unsigned* sb;
+    const float* bias;
+    int64_t M, N, K, lda, ldb, ldc, ldsa, ldsb;  // lda and ldb in bytes
+    int has_bias, relu, accum, c_type;
+    // the fast kernels
+    int c_vec;                       // C's rows at multiples of 16 bytes
+    int tiles_m, tiles_n;
+    int group_m, super_m, super_n;   // tile order (tile_coords)
+    int split;                       // k ranges of a tile, summed by a second launch
+    float* ws;                       // their partial tiles
+};
+// any alignment, leading dimension and size
+int launch_fp4_generic(const Fp4Args& a, void* stream);
 
 // Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the
 // planner's choice, else a row of kFp8Tiles, kFp8Skinny or kFp8Generic; and
