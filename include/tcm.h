@@ -675,6 +675,8 @@ const char* tcm_status_string(int status);
  *   "fp8_split"    0 = planner decides, else the k ranges each of its tiles
  *                  is cut into (1..64, at most one a 128-wide block and as
  *                  many as a launch holds).
+ *   "fp4_config"   tcm_gemm_mxfp4's kernel, numbered as fp8_config's.
+ *   "fp4_split"    as fp8_split, at most one a 256-wide step.
  * Unknown keys or out-of-range values: TCM_ERR_INVALID_VALUE.
  * tcm_get_option returns the value, or -2 for an unknown key.
  */

@@ -191,13 +191,33 @@ struct Fp4Args {
 };
 // any alignment, leading dimension and size
 int launch_fp4_generic(const Fp4Args& a, void* stream);
+// Macro tiles of the tiled kernel: waves WM x WN of (BM/WM) x 64 outputs, LDS stages of 256 k.
+struct Fp4Tile {
+    int bm, bn, wm, wn, stages;
+};
+constexpr int kNumFp4Tiles = 4;
+constexpr Fp4Tile kFp4Tiles[kNumFp4Tiles] = {
+    {256, 256, 2, 4, 2},  // large products: 128 x 64 a wave, two waves a SIMD
+    {256, 128, 4, 2, 3},  // half as many columns, three stages
+    {128, 128, 2, 2, 2},  // two workgroups a CU
+    {64, 128, 2, 2, 3},   // few rows
+};
+// A, B and sizes as fp4_tiles_fit accepts
+int launch_fp4_tile(int cfg, const Fp4Args& a, void* stream);
+// A few rows: workgroups of kFp4SkinnyCols columns by up to kFp4SkinnyRows
+// rows (`rows`, a row block; a.tiles_m of them), a.split k ranges.
+constexpr int kFp4SkinnyCols = 16, kFp4SkinnyRows = 64;
+int launch_fp4_skinny(int rows, const Fp4Args& a, void* stream);
 
 // Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the
 // planner's choice, else a row of kFp8Tiles, kFp8Skinny or kFp8Generic; and
 // the k ranges of a tile, 0 the planner's choice.
 constexpr int kFp8Skinny = kNumFp8Tiles, kFp8Generic = kNumFp8Tiles + 1, kFp8MaxSplit = 64;
+// and the same of tcm_gemm_mxfp4
+constexpr int kFp4Skinny = kNumFp4Tiles, kFp4Generic = kNumFp4Tiles + 1, kFp4MaxSplit = 64;
 struct LowpOpts {
     int fp8_config = -1, fp8_split = 0;
+    int fp4_config = -1, fp4_split = 0;
 };
 LowpOpts lowp_opts();
 // Shared with the C ABI's other entry points (tcm_api.cpp): the stream's

@@ -91,6 +91,73 @@ int mx_dequantize_impl(int64_t rows, int64_t cols, const void* q, int64_t ldq, c
     return done(launch_mx_dequantize(dtype, a, stream));
 }
 
+// Sizes, strides and alignment that the fast kernels take: 16-byte rows of A
+// and B, and a macro tile's rows within a buffer descriptor's range (2^30).
+bool fp4_tiles_fit(const Fp4Args& a) {
+    const int64_t lim = ((int64_t)1 << 30) / 256;
+    return a.K > 0 && !((uintptr_t)a.A & 15) && !((uintptr_t)a.B & 15) && !(a.lda & 15) && !(a.ldb & 15) && a.lda < lim && a.ldb < lim;
+}
+// The macro tile and the k ranges of a product by a model of its time, in
+// microseconds: the launch; for every round of workgroups a fill of its
+// pipelines and its K-steps, whose time grows from `lone` to `shared` as the
+// chip fills, or the operands' way from memory where that is longer; C's or
+// the partial tiles' way out; and for a split the sum's launch, each share's
+// part of it and the partial tiles' way back.
+struct Fp4Plan {
+    int config, split;
+};
+Fp4Plan plan_fp4(const Fp4Args& a, const LowpOpts& o) {
+    static constexpr struct {
+        int per_cu;
+        double lone, shared;
+    } kStep[kNumFp4Tiles] = {{1, 1.28, 1.65}, {1, 0.66, 0.93}, {2, 0.69, 1.04}, {2, 0.38, 0.63}};
+    // a launch counts its threads in 32 bits: so many workgroups of a product, at most 512 threads each, and of a sum, 256
+    // threads for 1024 outputs
+    constexpr int64_t kMaxWgs = (int64_t)1 << 22, kMaxSums = ((int64_t)1 << 24) - 1;
+    constexpr double kFixed = 3.0, kRound = 3.0, kSum = 2.5, kShare = 0.25, kBytesPerUs = 5e6;
+    Fp4Plan best{kFp4Generic, 1};
+    if (!fp4_tiles_fit(a) || o.fp4_config == kFp4Generic) return best;
+    const int64_t steps = (a.K + 255) / 256;
+    const double memory = (double)(a.M + a.N) * (double)a.K * 0.53 / kBytesPerUs;
+    double best_t = 1e30;
+    const int forced = o.fp4_config;
+    for (int c = 0; c < kNumFp4Tiles; ++c) {
+        if (forced >= 0 && forced < kNumFp4Tiles && c != forced) continue;
+        const Fp4Tile& t = kFp4Tiles[c];
+        const int64_t tiles = ((a.M + t.bm - 1) / t.bm) * ((a.N + t.bn - 1) / t.bn);
+        const int64_t slots = 256 * kStep[c].per_cu;
+        const bool sums = tiles * (t.bm * t.bn / 1024) <= kMaxSums;
+        const int64_t most = std::min({sums ? (int64_t)kFp4MaxSplit : 1, steps, (kMaxWgs - 1) / tiles});
+        for (int s = 1; s <= most; ++s) {
+            if (o.fp4_split && s != std::min<int64_t>(o.fp4_split, most)) continue;
+            const int64_t wgs = tiles * s, rest = wgs % slots;
+            const double step = (double)(wgs / slots) * kStep[c].shared +
+                                (rest == 0 ? 0 : kStep[c].lone + (kStep[c].shared - kStep[c].lone) * (double)rest / (double)slots);
+            const double rounds = (double)((wgs + slots - 1) / slots);
+            const double out = (double)wgs * t.bm * t.bn * (s > 1 ? 4 : c_elem_bytes(a.c_type)) / kBytesPerUs;
+            const double time = kFixed + std::max(rounds * kRound + (double)((steps + s - 1) / s) * step, memory) + out +
+                                (s > 1 ? kSum + kShare * s + 4.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            if (time < best_t) best_t = time, best = {c, s};
+        }
+    }
+    // Few rows: a workgroup's waves take a step each at a time, rows cost reads of A from the caches.
+    if (forced < 0 ? a.M <= kFp4SkinnyRows : forced == kFp4Skinny) {
+        static constexpr double kBlock[4] = {0.87, 1.4, 1.75, 2.6};
+        const int64_t blocks_m = (a.M + kFp4SkinnyRows - 1) / kFp4SkinnyRows;
+        const int64_t wgs = blocks_m * ((a.N + kFp4SkinnyCols - 1) / kFp4SkinnyCols);
+        const double round = kBlock[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
+        // (1024 outputs a workgroup: the sum's launch holds what this one does)
+        const int64_t most = std::min({(int64_t)kFp4MaxSplit, steps, (kMaxWgs - 1) / wgs});
+        for (int s = 1; s <= most; ++s) {
+            if (o.fp4_split && s != std::min<int64_t>(o.fp4_split, most)) continue;
+            const double time = kFixed + std::max((double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round, memory) +
+                                (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            if (time < best_t || forced == kFp4Skinny && best.config != kFp4Skinny) best_t = time, best = {kFp4Skinny, s};
+        }
+    }
+    return best;
+}
+
 int gemm_mx_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const uint32_t* sa, int64_t ldsa, const void* B,
                  int64_t ldb, const uint32_t* sb, int64_t ldsb, void* C, int64_t ldc, int dtype, const float* bias, int epilogue,
                  void* stream) {
@@ -135,14 +202,40 @@ int gemm_mx_impl(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
     a.accum = (epilogue & TCM_EPI_ACCUM) != 0;
     a.c_type = c_type;
     a.c_vec = ((uintptr_t)C & 15) == 0 && ((ldc * c_elem_bytes(c_type)) & 15) == 0;
-    // (a launch counts its threads in 32 bits)
-    if (((M + 63) / 64) * ((N + 63) / 64) >= ((int64_t)1 << 24)) return TCM_ERR_NOT_SUPPORTED;
+    const Fp4Plan pl = plan_fp4(a, lowp_opts());
+    if (pl.config == kFp4Generic) {
+        // (a launch counts its threads in 32 bits)
+        if (((M + 63) / 64) * ((N + 63) / 64) >= ((int64_t)1 << 24)) return TCM_ERR_NOT_SUPPORTED;
+        set_last_plan(
+            [](char* buf, size_t n, const int64_t* v) {
+                snprintf(buf, n, "kernel=fp4_generic M=%lld N=%lld K=%lld", (long long)v[0], (long long)v[1], (long long)v[2]);
+            },
+            {M, N, K});
+        return done(launch_fp4_generic(a, stream));
+    }
+    const bool skinny = pl.config == kFp4Skinny;
+    const int64_t blocks_m = (M + kFp4SkinnyRows - 1) / kFp4SkinnyRows;
+    const Fp4Tile t = skinny ? Fp4Tile{(int)((M + blocks_m * 16 - 1) / (blocks_m * 16)) * 16, kFp4SkinnyCols, 1, 1, 0} : kFp4Tiles[pl.config];
+    const int64_t tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
+    a.tiles_m = (int)tm;
+    a.tiles_n = (int)tn;
+    a.group_m = 4;
+    tile_order_shape(a.tiles_m, a.tiles_n, a.group_m, &a.super_m, &a.super_n);
+    a.split = pl.split;
+    std::unique_lock<std::mutex> order;
+    if (a.split > 1) {
+        void* ws = nullptr;
+        const int st = workspace_for(stream, (skinny ? M * N : tm * tn * t.bm * t.bn) * a.split * 4, &ws, &order);
+        if (st != TCM_OK) return st;
+        a.ws = (float*)ws;
+    }
     set_last_plan(
         [](char* buf, size_t n, const int64_t* v) {
-            snprintf(buf, n, "kernel=fp4_generic M=%lld N=%lld K=%lld", (long long)v[0], (long long)v[1], (long long)v[2]);
+            snprintf(buf, n, "kernel=fp4_%s tile=%dx%d tiles=%lld split=%d M=%lld N=%lld K=%lld", v[0] ? "skinny" : "tile", (int)v[1],
+                     (int)v[2], (long long)v[3], (int)v[4], (long long)v[5], (long long)v[6], (long long)v[7]);
         },
-        {M, N, K});
-    return done(launch_fp4_generic(a, stream));
+        {skinny, t.bm, t.bn, tm * tn, a.split, M, N, K});
+    return done(skinny ? launch_fp4_skinny(t.bm, a, stream) : launch_fp4_tile(pl.config, a, stream));
 }
 
 }  // namespace

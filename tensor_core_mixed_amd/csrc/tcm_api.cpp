@@ -635,6 +635,12 @@ int tcm_set_option(const char* key, int64_t value) {
     } else if (!strcmp(key, "fp8_split")) {
         if (value < 0 || value > kFp8MaxSplit) return TCM_ERR_INVALID_VALUE;
         g_lowp.fp8_split = (int)value;
+    } else if (!strcmp(key, "fp4_config")) {
+        if (value < -1 || value > kFp4Generic) return TCM_ERR_INVALID_VALUE;
+        g_lowp.fp4_config = (int)value;
+    } else if (!strcmp(key, "fp4_split")) {
+        if (value < 0 || value > kFp4MaxSplit) return TCM_ERR_INVALID_VALUE;
+        g_lowp.fp4_split = (int)value;
     } else {
         return TCM_ERR_INVALID_VALUE;
     }
@@ -658,6 +664,8 @@ int64_t tcm_get_option(const char* key) {
     if (!strcmp(key, "gemv_wide")) return g_opts.gemv_wide;
     if (!strcmp(key, "fp8_config")) return g_lowp.fp8_config;
     if (!strcmp(key, "fp8_split")) return g_lowp.fp8_split;
+    if (!strcmp(key, "fp4_config")) return g_lowp.fp4_config;
+    if (!strcmp(key, "fp4_split")) return g_lowp.fp4_split;
     return -2;
 }
 

@@ -180,6 +180,47 @@ def test_gemm(M, N, K, c_type):
     check_gemm(M, N, K, c_type, bias=K % 2 == 1, relu=M % 2 == 0)
 
 
+class forced:
+    def __init__(self, **options):
+        self.options = options
+
+    def __enter__(self):
+        for k, v in self.options.items():
+            assert T.tcm_set_option(k, v) == T.TCM_OK
+
+    def __exit__(self, *_):
+        for k in self.options:
+            T.tcm_set_option(k, -1 if k.endswith("config") else 0)
+
+
+KERNELS = {0: "tile=256x256", 1: "tile=256x128", 2: "tile=128x128", 3: "tile=64x128", 4: "fp4_skinny", 5: "fp4_generic"}
+
+
+@pytest.mark.parametrize("config", list(KERNELS))
+@pytest.mark.parametrize("M,N,K", SIZES + [(300, 520, 1024), (257, 513, 1281), (512, 256, 2304)])
+@pytest.mark.parametrize("c_type", [torch.float32, torch.bfloat16])
+def test_gemm_every_kernel(config, M, N, K, c_type):
+    with forced(fp4_config=config):
+        assert KERNELS[config] in check_gemm(M, N, K, c_type, bias=True, accum=K % 2 == 0, pad=(1, 2, 8 if M % 2 else 5))
+
+
+@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("split", [2, 3, 7, 64])
+@pytest.mark.parametrize("M,N,K", [(33, 70, 255), (65, 129, 1300), (300, 260, 2049), (20, 50, 20000)])
+@pytest.mark.parametrize("c_type", [torch.float32, torch.float16])
+def test_gemm_split(config, split, M, N, K, c_type):
+    with forced(fp4_config=config, fp4_split=split):
+        plan = check_gemm(M, N, K, c_type, bias=True, accum=True, relu=True)
+        assert KERNELS[config] in plan and f"split={min(split, -(-K // 256))} " in plan
+
+
+@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+def test_gemm_nan_scales_of_every_kernel(config):
+    with forced(fp4_config=config):
+        test_gemm_nan_scales()
+        test_gemm_scales_of_the_whole_range()
+
+
 @pytest.mark.parametrize("shift,align,pad", [(1, 1, (1, 2, 3)), (0, 1, (0, 0, 0)), (8, 8, (3, 0, 1)), (0, 16, (5, 1, 1))])
 @pytest.mark.parametrize("c_type", TYPES)
 def test_gemm_any_alignment(shift, align, pad, c_type):

@@ -76,3 +76,16 @@ def test_gemm_empty(kw):
 def test_gemm_types_stay_out_of_the_other_entry_points():
     assert T.tcm_gemm(8, 8, 8, X, 8, Y, 8, Z, 8, T.TCM_MXFP4_F32, None, 0, None) == INV
     assert T.tcm_gemm_fp8(8, 8, 8, X, 8, S, 8, Y, 8, ST, 1, Z, 8, T.TCM_MXFP4_F32, None, 0, None) == INV
+
+
+@pytest.mark.parametrize("key,default,allowed,refused", [
+    ("fp4_config", -1, (-1, 0, 3, 4, 5), (-2, 6, 1 << 32)), ("fp4_split", 0, (0, 1, 64), (-1, 65, 1 << 32))])
+def test_options(key, default, allowed, refused):
+    assert T.tcm_get_option(key) == default
+    try:
+        for value in allowed:
+            assert T.tcm_set_option(key, value) == OK and T.tcm_get_option(key) == value
+        for value in refused:
+            assert T.tcm_set_option(key, value) == INV and T.tcm_get_option(key) == allowed[-1]
+    finally:
+        assert T.tcm_set_option(key, default) == OK
