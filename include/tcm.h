@@ -613,6 +613,41 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
                        const int32_t* counts, const float* dlosses,
                        void* D, int64_t ldd, void* stream);
 
+/*
+ * tcm_orthogonalize -- Newton-Schulz steps that bring each of `batch` matrices
+ * near its nearest orthogonal one (a momentum's update of a weight, as the
+ * Muon optimiser makes it),
+ *
+ *     X = G / (|G| + eps),   |G| the root of the sum of squares,
+ *     X <- a X + (b X X^T + c (X X^T)^2) X   with each step's own a, b, c,
+ *     O = scale * X.
+ *
+ * The steps take every singular value s to a s + b s^3 + c s^5 and keep the
+ * singular vectors.  (rows > cols: the same on the transposed matrix.)
+ *
+ *   G, ldg, stride_g   batch matrices rows x cols, row-major, ldg >= cols,
+ *                entry e at G + e * stride_g elements; f16, bf16 or f32 by
+ *                `dtype`.  0 <= stride_g, stride_o < 2^40.
+ *   O, ldo, stride_o   the same of O, in f32 or by TCM_C_F16 / TCM_C_BF16
+ *                rounded to nearest even.  Entries must not overlap each other
+ *                (stride_o >= (rows-1)*ldo + cols) or G.
+ *   steps, coefficients   3 * steps floats in HOST memory, read during the
+ *                call; steps >= 0 (0: O = scale * G / (|G| + eps)).
+ *   eps          >= 0; above 0 it keeps a matrix of zeros one of zeros.
+ * Products run on the matrix cores in two binary16 parts of each value, which
+ * keep 22 bits, and add in binary32; scales from the coefficients keep them
+ * within range.  The result is as exact as with binary32 products.  The sum of
+ * squares is a binary64 one.  A NaN makes its entry NaN, and so does an
+ * infinity (with no steps its own value only, and zeros of the others).  Any
+ * alignment.  rows and cols up to 2^20 - 32 (else TCM_ERR_NOT_SUPPORTED).
+ * Returns as tcm_gemm; the workspace rules are tcm_gemm's (it holds G five
+ * times in f32's size, for as many entries as 2 GiB take, one at least).
+ */
+int tcm_orthogonalize(int64_t batch, int64_t rows, int64_t cols,
+                      const void* G, int64_t ldg, int64_t stride_g,
+                      void* O, int64_t ldo, int64_t stride_o, int dtype,
+                      int steps, const float* coefficients, float eps, float scale, void* stream);
+
 /* Text of a status code (static storage; never NULL). */
 const char* tcm_status_string(int status);
 

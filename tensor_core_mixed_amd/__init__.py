@@ -93,6 +93,8 @@ def lib():
         L.tcm_moe_balance.restype = ci
         L.tcm_moe_route_grad.argtypes = [i64, i64, i64, vp, i64, ci, ctypes.c_float, vp, vp, vp, vp, vp, vp, i64, vp]
         L.tcm_moe_route_grad.restype = ci
+        L.tcm_orthogonalize.argtypes = [i64, i64, i64, vp, i64, i64, vp, i64, i64, ci, ci, vp, ctypes.c_float, ctypes.c_float, vp]
+        L.tcm_orthogonalize.restype = ci
         L.tcm_status_string.argtypes = [ci]
         L.tcm_status_string.restype = ctypes.c_char_p
         L.tcm_set_option.argtypes = [ctypes.c_char_p, i64]
@@ -314,6 +316,16 @@ def tcm_moe_route_grad(tokens, experts, topk, logits, ldx, dtype, scale, ids, ma
     the tcm status code."""
     return lib().tcm_moe_route_grad(tokens, experts, topk, logits, ldx, dtype, scale, ids, mask, dweights, counts, dlosses, D, ldd,
                                     stream)
+
+
+def tcm_orthogonalize(batch, rows, cols, G, ldg, stride_g, O, ldo, stride_o, dtype, coefficients, eps, scale, stream):
+    """Newton-Schulz steps on `batch` matrices; `coefficients`: a, b, c of
+    each step in a flat sequence.  Returns the tcm status code."""
+    n = len(coefficients)
+    if n % 3:
+        raise ValueError("three coefficients a step")
+    return lib().tcm_orthogonalize(batch, rows, cols, G, ldg, stride_g, O, ldo, stride_o, dtype, n // 3,
+                                   (ctypes.c_float * n)(*coefficients), eps, scale, stream)
 
 
 def tcm_version():

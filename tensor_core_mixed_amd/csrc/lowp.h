@@ -209,6 +209,54 @@ int launch_fp4_tile(int cfg, const Fp4Args& a, void* stream);
 constexpr int kFp4SkinnyCols = 16, kFp4SkinnyRows = 64;
 int launch_fp4_skinny(int rows, const Fp4Args& a, void* stream);
 
+// ---- Newton-Schulz steps (tcm_orthogonalize)
+
+// Macro tiles of its products: waves WM x WN of (BM/WM) x 64 outputs, LDS stages of 32 k in two parts.
+struct OrthoTile {
+    int bm, bn, wm, wn, stages, per_cu;
+};
+constexpr int kNumOrthoTiles = 2;
+constexpr OrthoTile kOrthoTiles[kNumOrthoTiles] = {
+    {256, 256, 2, 4, 2, 1},  // large products
+    {128, 128, 2, 2, 2, 2},
+};
+// sizes up to 2^20 - 32 (a tile's rows stay within a buffer descriptor's range), workspace of the entries of a launch, slices
+// of a sum of squares
+constexpr int64_t kOrthoMaxSize = ((int64_t)1 << 20) - 32, kOrthoWorkspace = (int64_t)2 << 30, kOrthoSlices = 256;
+struct OrthoArgs {
+    const void* g;         // [rows][cols]
+    int64_t batch, rows, cols, ldg, stride_g;
+    void* o;
+    int64_t ldo, stride_o;
+    int o_type;
+    float eps;
+    int64_t rows_pad, cols_pad;  // to whole pieces of 32
+    int64_t slices;        // of an entry's sum of squares
+    double* squares;       // [batch][slices]
+    char* as_is;           // parts of G over its norm [rows][cols_pad], entry_bytes apart
+    char* across;          // and transposed [cols][rows_pad]
+    int64_t entry_bytes;
+    int64_t first_tile;    // of a launch
+};
+// G's norm, then factor * G / (norm + eps): its parts, or with `out` O
+int launch_ortho_start(int x_type, const OrthoArgs& a, float factor, bool out, void* stream);
+
+// alpha * A B^T + beta * P of every entry, in parts: A [M][k_pad], B [N][k_pad], P and D [M][n_pad], E [N][m_pad]
+// transposed; or to out.
+struct OrthoMul {
+    const char *A, *B, *P;
+    char *D, *E;
+    int64_t entry_bytes, M, N, k_pad, n_pad, m_pad;
+    float alpha, beta;
+    char* out;             // [M][N], or with out_across [N][M], of out_type; or null
+    int64_t ld_out, stride_out;
+    int out_type, out_across;
+    int batch, symmetric;
+    int tiles, tiles_m, tiles_n, group_m, super_m, super_n, split;
+    float* ws;             // partial tiles
+};
+int launch_ortho_mul(int cfg, const OrthoMul& p, void* stream);
+
 // Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the
 // planner's choice, else a row of kFp8Tiles, kFp8Skinny or kFp8Generic; and
 // the k ranges of a tile, 0 the planner's choice.

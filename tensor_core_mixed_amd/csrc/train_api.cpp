@@ -1,8 +1,9 @@
-// C ABI of the router's losses and gradient (declared in include/tcm.h):
-// argument checks and dispatch.
+// C ABI of the router's losses and gradient and of the orthogonalised update
+// (declared in include/tcm.h): argument checks and dispatch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 
 #include "api_util.h"
@@ -112,6 +113,190 @@ int route_grad_impl(int64_t tokens, int64_t experts, int64_t topk, const void* l
     return done(launch_route_grad(t, a, stream));
 }
 
+// The largest |f| among [0, r] of f(s) = a s + b s^3 + c s^5 (in t = s^2: at the ends and where a + 3 b t + 5 c t^2 = 0)
+double largest_step(double a, double b, double c, double r) {
+    const auto f = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + t * c))); };
+    double most = f(r * r);
+    const auto at = [&](double t) {
+        if (t > 0 && t < r * r) most = std::max(most, f(t));
+    };
+    if (c != 0) {
+        const double d = 9 * b * b - 20 * a * c;
+        if (d >= 0) {
+            at((-3 * b + std::sqrt(d)) / (10 * c));
+            at((-3 * b - std::sqrt(d)) / (10 * c));
+        }
+    } else if (b != 0) {
+        at(-a / (3 * b));
+    }
+    return most;
+}
+// and of f(s) = b s + c s^2
+double largest_square(double b, double c, double r) {
+    const auto f = [&](double s) { return std::fabs(s * (b + s * c)); };
+    double most = f(r);
+    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < r) most = std::max(most, f(-b / (2 * c)));
+    return most;
+}
+// The exponent that takes values up to `most` near 2^14, a quarter of binary16's largest.  (A bound that is not finite,
+// or far outside binary32's middle, has values that are none either.)
+int exponent_for(double most) {
+    if (!(most > 0x1p-60)) return 60;
+    if (!(most < 0x1p60)) return -60;
+    return 13 - std::ilogb(most);
+}
+
+int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t ldg, int64_t stride_g, void* o, int64_t ldo,
+               int64_t stride_o, int dtype, int steps, const float* coef, float eps, float scale, void* stream) {
+    const int t = dtype & 0xff, flags = dtype & ~0xff;
+    if (t != F16 && t != BF16 && t != F32) return TCM_ERR_INVALID_VALUE;
+    if ((flags & ~(TCM_C_F16 | TCM_C_BF16)) || ((flags & TCM_C_F16) && (flags & TCM_C_BF16))) return TCM_ERR_INVALID_VALUE;
+    if (batch < 0 || rows < 0 || cols < 0 || batch >= kDim || rows >= kDim || cols >= kDim) return TCM_ERR_INVALID_VALUE;
+    if (ldg < std::max<int64_t>(cols, 1) || ldo < std::max<int64_t>(cols, 1)) return TCM_ERR_INVALID_VALUE;
+    if (stride_g < 0 || stride_o < 0 || stride_g >= ((int64_t)1 << 40) || stride_o >= ((int64_t)1 << 40)) return TCM_ERR_INVALID_VALUE;
+    if (steps < 0 || (steps > 0 && !coef) || !(eps >= 0)) return TCM_ERR_INVALID_VALUE;
+    if (batch == 0 || rows == 0 || cols == 0) {
+        set_last_plan("empty problem");
+        return TCM_OK;
+    }
+    if (!g || !o) return TCM_ERR_INVALID_VALUE;
+    const int o_type = (flags & TCM_C_F16) ? C_F16 : ((flags & TCM_C_BF16) ? C_BF16 : C_ACC);
+    const int64_t ge = span_of(rows, cols, ldg, 1), oe = span_of(rows, cols, ldo, 1);
+    if (ge < 0 || oe < 0 || (batch > 1 && stride_o < oe)) return TCM_ERR_INVALID_VALUE;
+    const int64_t gb = span_of(batch, ge, stride_g, elem_bytes(t)), ob = span_of(batch, oe, stride_o, c_elem_bytes(o_type));
+    if (batch > 1 && stride_g > (((int64_t)1 << 60) - ge) / (batch - 1)) return TCM_ERR_INVALID_VALUE;
+    if (gb < 0 || ob < 0) return TCM_ERR_INVALID_VALUE;
+    const Region out[1] = {{o, ob}}, in[1] = {{g, gb}};
+    if (!disjoint(out, in)) return TCM_ERR_INVALID_VALUE;
+    if (std::max(rows, cols) > kOrthoMaxSize) return TCM_ERR_NOT_SUPPORTED;
+
+    const bool tall = rows > cols;
+    const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
+    const auto pad = [](int64_t x) { return (x + 31) / 32 * 32; };
+    const auto line = [](int64_t x) { return (x + 255) / 256 * 256; };
+    // an entry's parts: X, X transposed twice (read by other tiles while the next is written), S, T
+    const int64_t x_bytes = line(n * pad(m) * 4), xt_bytes = line(m * pad(n) * 4), s_bytes = line(n * pad(n) * 4);
+    const int64_t entry = steps ? x_bytes + 2 * xt_bytes + 2 * s_bytes : 0;
+    // The tile and the k ranges of a product, by the workgroups that the chip holds at once.
+    struct Plan {
+        int cfg, tiles_m, tiles_n, tiles, split;
+        int64_t ws;
+    };
+    const auto plan = [&](int64_t M, int64_t N, int64_t K, int64_t entries, bool sym) {
+        Plan best{};
+        for (int c = 0; c < kNumOrthoTiles; ++c) {
+            const OrthoTile& x = kOrthoTiles[c];
+            const int64_t tm = (M + x.bm - 1) / x.bm, tn = (N + x.bn - 1) / x.bn, tiles = sym ? tm * (tm + 1) / 2 : tm * tn;
+            const int64_t slots = 256 * x.per_cu, all = tiles * entries, ksteps = pad(K) / 32;
+            const int64_t split = std::max<int64_t>(1, std::min({slots / all, ksteps / 4, (int64_t)16}));
+            best = Plan{c, (int)tm, (int)tn, (int)tiles, (int)split, split > 1 ? all * split * x.bm * x.bn * 4 : 0};
+            if (all >= 192) break;
+        }
+        return best;
+    };
+    // entries in parts of a call, so that the workspace stays within bounds and a launch within its 32 bits of threads
+    const int64_t tiles = std::max(((n + 127) / 128) * ((m + 127) / 128), ((n + 63) / 64) * ((m + 63) / 64));
+    const int64_t chunk = std::min({batch, std::max<int64_t>(1, kOrthoWorkspace / std::max<int64_t>(entry, 1)), std::max<int64_t>(1, ((int64_t)1 << 22) / tiles)});
+    const Plan ps = plan(n, n, m, chunk, true), pt = plan(n, n, n, chunk, true), px = plan(n, m, n, chunk, false);
+    const int64_t slices = std::min<int64_t>(kOrthoSlices, (rows * ((cols + 7) / 8) + 1023) / 1024);
+    const int64_t squares = line(chunk * slices * 8), partial = std::max({ps.ws, pt.ws, px.ws});
+    void* ws = nullptr;
+    std::unique_lock<std::mutex> order;
+    const int st = workspace_for(stream, squares + chunk * entry + partial, &ws, &order);
+    if (st != TCM_OK) return st;
+    set_last_plan(
+        [](char* buf, size_t len, const int64_t* v) {
+            snprintf(buf, len, "kernel=ortho batch=%lld rows=%lld cols=%lld dtype=%d steps=%d chunk=%lld tile=%d,%d,%d split=%lld", (long long)v[0],
+                     (long long)v[1], (long long)v[2], (int)v[3], (int)v[4], (long long)v[5], (int)(v[6] / 100), (int)(v[6] / 10 % 10),
+                     (int)(v[6] % 10), (long long)v[7]);
+        },
+        {batch, rows, cols, t, steps, chunk, 100 * ps.cfg + 10 * pt.cfg + px.cfg, ps.split * 10000 + pt.split * 100 + px.split});
+    for (int64_t b = 0; b < batch; b += chunk) {
+        const int64_t count = std::min(chunk, batch - b);
+        char* base = (char*)ws + squares;
+        char *x = base, *xt[2] = {base + x_bytes, base + x_bytes + xt_bytes}, *sq = base + x_bytes + 2 * xt_bytes, *tt = sq + s_bytes;
+        OrthoArgs a{};
+        a.g = (const char*)g + b * stride_g * elem_bytes(t);
+        a.batch = count;
+        a.rows = rows;
+        a.cols = cols;
+        a.ldg = ldg;
+        a.stride_g = stride_g;
+        a.o = (char*)o + b * stride_o * c_elem_bytes(o_type);
+        a.ldo = ldo;
+        a.stride_o = stride_o;
+        a.o_type = o_type;
+        a.eps = eps;
+        a.rows_pad = pad(rows);
+        a.cols_pad = pad(cols);
+        a.slices = slices;
+        a.squares = (double*)ws;
+        a.as_is = tall ? xt[0] : x;
+        a.across = tall ? x : xt[0];
+        a.entry_bytes = entry;
+        double most = 1.001;  // of X's singular values (the norm bounds them)
+        int ex = exponent_for(most);
+        if (launch_ortho_start(t, a, steps ? (float)std::ldexp(1.0, ex) : scale, steps == 0, stream) != 0) return TCM_ERR_HIP;
+        for (int k = 0; k < steps; ++k) {
+            const double ca = coef[3 * k], cb = coef[3 * k + 1], cc = coef[3 * k + 2];
+            const int es = exponent_for(most * most), et = exponent_for(largest_square(cb, cc, most * most) * 1.001);
+            const auto two = [](double v, int e) { return (float)std::ldexp(v, e); };
+            const auto mul = [&](const Plan& p, int64_t M, int64_t N, int64_t K, bool sym) {
+                OrthoMul q{};
+                q.entry_bytes = entry;
+                q.M = M;
+                q.N = N;
+                q.k_pad = pad(K);
+                q.n_pad = pad(N);
+                q.m_pad = pad(M);
+                q.batch = (int)count;
+                q.symmetric = sym;
+                q.tiles = p.tiles;
+                q.tiles_m = p.tiles_m;
+                q.tiles_n = p.tiles_n;
+                q.group_m = 4;
+                tile_order_shape(q.tiles_m, q.tiles_n, q.group_m, &q.super_m, &q.super_n);
+                q.split = p.split;
+                q.ws = (float*)(base + chunk * entry);
+                return q;
+            };
+            OrthoMul q = mul(ps, n, n, m, true);  // S
+            q.A = q.B = x;
+            q.D = q.E = sq;
+            q.alpha = two(1, es - 2 * ex);
+            if (launch_ortho_mul(ps.cfg, q, stream) != 0) return TCM_ERR_HIP;
+            q = mul(pt, n, n, n, true);  // T
+            q.A = q.B = q.P = sq;
+            q.D = q.E = tt;
+            q.alpha = two(cc, et - 2 * es);
+            q.beta = two(cb, et - es);
+            if (launch_ortho_mul(pt.cfg, q, stream) != 0) return TCM_ERR_HIP;
+            most = largest_step(ca, cb, cc, most) * 1.001;
+            const bool end = k == steps - 1;
+            const int next = end ? 0 : exponent_for(most);
+            const double f = end ? (double)scale : 1.0;
+            q = mul(px, n, m, n, false);  // X
+            q.A = tt;
+            q.B = xt[k & 1];
+            q.P = x;
+            q.D = x;
+            q.E = xt[~k & 1];
+            q.alpha = two(f, next - et - ex);
+            q.beta = two(f * ca, next - ex);
+            if (end) {
+                q.out = (char*)a.o;
+                q.ld_out = ldo;
+                q.stride_out = stride_o;
+                q.out_type = o_type;
+                q.out_across = tall;
+            }
+            if (launch_ortho_mul(px.cfg, q, stream) != 0) return TCM_ERR_HIP;
+            ex = next;
+        }
+    }
+    return TCM_OK;
+}
+
 }  // namespace
 }  // namespace tcm
 
@@ -129,6 +314,13 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk, const void
                        void* D, int64_t ldd, void* stream) {
     return guarded([&] {
         return route_grad_impl(tokens, experts, topk, logits, ldx, dtype, scale, ids, mask, dweights, counts, dlosses, D, ldd, stream);
+    });
+}
+
+int tcm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void* G, int64_t ldg, int64_t stride_g, void* O, int64_t ldo,
+                      int64_t stride_o, int dtype, int steps, const float* coefficients, float eps, float scale, void* stream) {
+    return guarded([&] {
+        return ortho_impl(batch, rows, cols, G, ldg, stride_g, O, ldo, stride_o, dtype, steps, coefficients, eps, scale, stream);
     });
 }
 
