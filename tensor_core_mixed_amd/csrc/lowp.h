@@ -102,8 +102,7 @@ struct BalanceArgs {
     float* p;              // [groups][experts]
     int* n;                // [groups][experts + 1]
     double* z;             // [groups]
-    double* share;         // [experts / 64]
-    int* arrived;
+    unsigned long long* arrived;
 };
 // a workgroup's waves in the two ways to run, and the most workgroups of the second
 constexpr int kBalanceWaves = 8, kBalanceOneWaves = 16, kBalanceGroups = 256, kBalanceOneTokens = 128;

@@ -242,8 +242,7 @@ struct Loop {
         if constexpr (FP4) f.s[j] = read_scales(s, l.sb + n_tile(j) * 4);
     }
     __device__ __forceinline__ static i8v wide(i4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
-    // products of a step that one accumulator takes
-    static constexpr int STEP = FP4 ? 2 : 3;
+    // product Q of those that one accumulator takes in a step
     template <int Q>
     __device__ __forceinline__ static f4 mma(f4 acc, const Cols& b, int j, const Rows& a, int i) {
         if constexpr (FP4) {
@@ -267,10 +266,6 @@ struct Loop {
         for (int i = 0; i < PER_SLOT; ++i)
             if (slot < SLOTS && slot * PER_SLOT + i < OPS) dma_op(d, s, slot * PER_SLOT + i, wave);
     }
-    static constexpr int slot_ops(int slot) {
-        return slot >= SLOTS || slot * PER_SLOT >= OPS ? 0 : (OPS - slot * PER_SLOT < PER_SLOT ? OPS - slot * PER_SLOT : PER_SLOT);
-    }
-
     struct Pipe {
         Rows fr[2];
         Cols fc;
@@ -289,6 +284,7 @@ struct Loop {
             Rows& cur = f.fr[g & 1];
             Rows& nxt = f.fr[(g + 1) & 1];
             const bool end = g == NG - 1;
+            __builtin_amdgcn_sched_barrier(0);  // (reads, copies and products stay within their group)
             if (!end) {
                 read_rows(nxt, s, l, g + 1);
             } else {
@@ -312,16 +308,6 @@ struct Loop {
                 }
                 if (end) read_col(f.fc, nx, l, j);
                 dma_slot(d, end ? s : before, slot, wave);
-                // in turn products, reads and copies
-#pragma unroll
-                for (int i = 0; i < GM; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, STEP, 0);
-                    if (end) __builtin_amdgcn_sched_group_barrier(0x100, FP4 ? 3 : 2, 0);
-                    else if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, FP4 ? 3 : 2, 0);
-                    if (i == 0 && slot_ops(slot) == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-                    if (i == 0 && slot_ops(slot) == 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
-                    if (i == 0 && slot_ops(slot) >= 3) __builtin_amdgcn_sched_group_barrier(0x020, 3, 0);
-                }
             }
         }
 #pragma unroll

@@ -44,15 +44,14 @@ int balance_impl(int64_t tokens, int64_t experts, int64_t topk, const void* logi
                    : (int)std::min<int64_t>(kBalanceGroups, (tokens + kBalanceWaves - 1) / kBalanceWaves);
     std::unique_lock<std::mutex> order;
     if (a.groups > 1) {
-        const int64_t joins = (experts + 63) / 64, g = a.groups;
+        const int64_t g = a.groups;
         void* ws = nullptr;
-        const int st = workspace_for(stream, 8 * g + 8 * joins + 4 * g * experts + 4 * g * (experts + 1) + 4, &ws, &order);
+        const int st = workspace_for(stream, 8 + 8 * g + 4 * g * experts + 4 * g * (experts + 1), &ws, &order);
         if (st != TCM_OK) return st;
-        a.z = (double*)ws;
-        a.share = a.z + g;
-        a.p = (float*)(a.share + joins);
+        a.arrived = (unsigned long long*)ws;
+        a.z = (double*)ws + 1;
+        a.p = (float*)(a.z + g);
         a.n = (int*)(a.p + g * experts);
-        a.arrived = a.n + g * (experts + 1);
     }
     set_last_plan(
         [](char* buf, size_t n, const int64_t* v) {
