@@ -334,47 +334,49 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
     }
 }
 
-// The partial sums of 64 experts a workgroup.  Their parts of sum n p / (T k T), which lies in [0, 1], are added as
-// integers of 2^-40 in the word that also counts the arrivals (and those with a NaN): one atomic addition hands
-// everything on, without a fence, and gives the same sum in any order.  (Loss: off by experts * 2^-41 * experts / 64 at
-// most, under half a step of binary32 near 1.)
-constexpr int kJoin = 16, kJoinRows = (kBalanceGroups + kJoin - 1) / kJoin, kFraction = 40, kNans = 48, kArrivals = 56;
-static_assert((kRouteMaxExperts + 63) / 64 <= 16, "counts of arrivals in 8 bits");
-__global__ __launch_bounds__(64 * kJoin) void balance_join_kernel(BalanceArgs a) {
-    __shared__ double sp[kJoin][64], sz[kBalanceGroups / 64];
-    __shared__ int sn[kJoin][64], sv[kBalanceGroups / 64];
-    const int tid = threadIdx.x, lane = tid & 63, g = tid >> 6, e = blockIdx.x * 64 + lane;
+// The partial sums of 16 experts a workgroup (of 64: 8.4 us of 16384 x 256's, five of them reading on four CUs).  Their
+// parts of sum n p / (T k T), which lies in [0, 1], are added as integers of 2^-40 in the word that also counts the
+// arrivals (and those with a NaN): one atomic addition hands everything on, without a fence, and gives the same sum in
+// any order.  (Loss: off by experts * 2^-41 * experts / 16 at most, about half a step of binary32 near 1.)
+constexpr int kJoinWaves = 16, kJoinExperts = 16, kJoinSlices = kJoinWaves * 4, kJoinRows = (kBalanceGroups + kJoinSlices - 1) / kJoinSlices;
+constexpr int kFraction = 40, kNans = 48, kArrivals = 56;
+static_assert((kRouteMaxExperts + kJoinExperts - 1) / kJoinExperts <= 128, "counts of arrivals in 8 bits");
+__global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(BalanceArgs a) {
+    __shared__ double sp[kJoinWaves][kJoinExperts], sz[kBalanceGroups / 64];
+    __shared__ int sn[kJoinWaves][kJoinExperts], sv[kBalanceGroups / 64];
+    const int tid = threadIdx.x, lane = tid & 63, g = tid >> 6, e = blockIdx.x * kJoinExperts + (lane & 15);
     double p = 0, z = 0;
     int n = 0, valid = 0;
-    if (tid < kBalanceGroups) {
-        if (tid < a.groups) z = a.z[tid], valid = a.n[(int64_t)tid * (a.experts + 1) + a.experts];
-    }
+    if (tid < a.groups) z = a.z[tid], valid = a.n[(int64_t)tid * (a.experts + 1) + a.experts];
     if (e < a.experts) {
         float x[kJoinRows];  // (in flight together)
         int y[kJoinRows];
 #pragma unroll
         for (int i = 0; i < kJoinRows; ++i) {
-            const int r = i * kJoin + g;
+            const int r = i * kJoinSlices + (tid >> 4);
             x[i] = r < a.groups ? a.p[(int64_t)r * a.experts + e] : 0.f;
             y[i] = r < a.groups ? a.n[(int64_t)r * (a.experts + 1) + e] : 0;
         }
 #pragma unroll
         for (int i = 0; i < kJoinRows; ++i) p += (double)x[i], n += y[i];
     }
-    sp[g][lane] = p;
-    sn[g][lane] = n;
+    p += __shfl_xor(p, 16);
+    p += __shfl_xor(p, 32);
+    n += __shfl_xor(n, 16);
+    n += __shfl_xor(n, 32);
+    if (lane < 16) sp[g][lane] = p, sn[g][lane] = n;
     if (tid < kBalanceGroups) {
         z = wave_sum(z);
         valid = wave_sum(valid);
         if (lane == 0) sz[g] = z, sv[g] = valid;
     }
     __syncthreads();
-    if (g != 0) return;
+    if (tid >= 16) return;
     p = 0, n = 0;
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i) p += sp[i][lane], n += sn[i][lane];
+    for (int i = 0; i < kJoinWaves; ++i) p += sp[i][lane], n += sn[i][lane];
     if (e < a.experts) a.counts[e] = n;
-    const double dot = wave_sum((double)n * p);
+    const double dot = row_sum((double)n * p);
     z = 0, valid = 0;
 #pragma unroll
     for (int i = 0; i < kBalanceGroups / 64; ++i) z += sz[i], valid += sv[i];
@@ -398,7 +400,8 @@ int balance_n(const BalanceArgs& a, hipStream_t s) {
         const dim3 grid((unsigned)a.groups), block(64 * kBalanceWaves);
         if (a.sigmoid) hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, true, false>), grid, block, 0, s, a);
         else hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, false, false>), grid, block, 0, s, a);
-        hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)((a.experts + 63) / 64)), dim3(64 * kJoin), 0, s, a);
+        hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)((a.experts + kJoinExperts - 1) / kJoinExperts)),
+                           dim3(64 * kJoinWaves), 0, s, a);
     }
     return (int)hipGetLastError();
 }
