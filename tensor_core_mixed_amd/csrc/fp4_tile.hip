@@ -41,7 +41,7 @@ struct Tile : pair::Loop<kFp4Tiles[CFG].bm, kFp4Tiles[CFG].bn, kFp4Tiles[CFG].wm
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
         const pair::Operands o{a.A, a.B, a.M, a.N, a.lda, a.ldb, mx_bytes(a.K), a.K, a.sa, a.sb, a.ldsa, a.ldsb};
-        if (k_lo < k_hi) L::run(acc, o, smem, m0, n0, k_lo, k_hi, wave, lane);
+        if (k_lo < k_hi) L::run(acc, o, smem, m0, n0, k_lo, k_hi, k_hi - k_lo, wave, lane);
         if (a.split > 1) {
             f4* w = (f4*)a.ws + ((int64_t)nidx * L::NW + wave) * FM * 4 * 64 + lane;
 #pragma unroll

@@ -210,14 +210,15 @@ int launch_fp4_skinny(int rows, const Fp4Args& a, void* stream);
 
 // ---- Newton-Schulz steps (tcm_orthogonalize)
 
-// Macro tiles of its products: waves WM x WN of (BM/WM) x 64 outputs, LDS stages of 32 k in two parts.
+// Macro tiles of its products: `parts` times waves WM x WN of (BM/WM) x 64 outputs, each part with its own share of k and
+// LDS stages of 32 k in two parts.
 struct OrthoTile {
-    int bm, bn, wm, wn, stages, per_cu;
+    int bm, bn, wm, wn, stages, parts;
 };
 constexpr int kNumOrthoTiles = 2;
 constexpr OrthoTile kOrthoTiles[kNumOrthoTiles] = {
     {256, 256, 2, 4, 2, 1},  // large products
-    {128, 128, 2, 2, 2, 2},
+    {128, 128, 2, 2, 2, 2},  // their sum over the two halves of k in LDS
 };
 // sizes up to 2^20 - 32 (a tile's rows stay within a buffer descriptor's range), workspace of the entries of a launch, slices
 // of a sum of squares

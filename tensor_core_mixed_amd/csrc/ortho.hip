@@ -27,7 +27,8 @@
 //         tiles leave as they are and transposed (through LDS, a wave its own
 //         64 x 32 values at a time) for the next step.
 //
-// Few tiles leave CUs without work: k is then cut into ranges, one a
+// Few tiles leave CUs without work: k is cut into two halves within a
+// workgroup of small tiles (their sum goes through LDS) and into ranges, one a
 // workgroup, and a second launch adds the partial tiles in order and finishes
 // them.
 #include <hip/hip_runtime.h>
@@ -190,8 +191,9 @@ template <int CFG>
 struct Tile {
     using L = pair::Loop<kOrthoTiles[CFG].bm, kOrthoTiles[CFG].bn, kOrthoTiles[CFG].wm, kOrthoTiles[CFG].wn, kOrthoTiles[CFG].stages, false,
                          false>;
-    static constexpr int FM = L::FM;
-    static_assert(FM % 2 == 0 && L::TM % 32 == 0, "a wave's rows in pairs of tiles");
+    static constexpr int FM = L::FM, PARTS = kOrthoTiles[CFG].parts, NT = L::NT * PARTS, LDS = L::LDS * PARTS;
+    static constexpr int FP = FM / PARTS;  // row tiles that a wave finishes
+    static_assert(FP % 2 == 0 && L::TM % 32 == 0, "a wave's rows in pairs of tiles");
     static constexpr int kPitch = 33, kWaveWords = 64 * kPitch;
 
     // Tile t of an entry's: all of them, or those on and under the diagonal.
@@ -278,11 +280,10 @@ struct Tile {
     }
 
     __device__ __forceinline__ static void run(const OrthoMul& p) {
-        __shared__ __attribute__((aligned(1024))) char smem_raw[L::LDS];
-        static_assert(L::NW * kWaveWords * 4 <= L::LDS, "");
-        pair::lds_char* smem = (pair::lds_char*)smem_raw;
+        __shared__ __attribute__((aligned(1024))) char smem_raw[LDS];
+        static_assert(L::NW * PARTS * kWaveWords * 4 <= LDS && (PARTS == 1 || NT * FP * 4 * 16 <= LDS), "");
         const int tid = threadIdx.x, lane = tid & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int id = __builtin_amdgcn_readfirstlane(tid >> 6), part = id / L::NW, wave = id % L::NW;
         const int wm = wave / L::WN, wn = wave % L::WN;
         const int nidx = xcd_order(blockIdx.x, p.tiles * p.split * p.batch);
         const int entry = nidx / (p.tiles * p.split), rest = nidx - entry * p.tiles * p.split;
@@ -291,7 +292,8 @@ struct Tile {
         tile_at(p, t, &tm, &tn);
         const int64_t m0 = (int64_t)tm * L::BM, n0 = (int64_t)tn * L::BN;
         const int64_t steps = p.k_pad / 32;
-        const int k_lo = (int)(share * steps / p.split), k_hi = (int)((share + 1) * steps / p.split);
+        const int lo = (int)(share * steps / p.split), hi = (int)((share + 1) * steps / p.split);
+        const int each = (hi - lo + PARTS - 1) / PARTS, k_lo = lo + part * each, k_hi = min(k_lo + each, hi);
         f4 acc[FM][4];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -299,23 +301,48 @@ struct Tile {
             for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
         const pair::Operands o{(const unsigned char*)p.A + entry * p.entry_bytes, (const unsigned char*)p.B + entry * p.entry_bytes, p.M, p.N,
                                p.k_pad * 4, p.k_pad * 4, p.k_pad * 4, 0, nullptr, nullptr, 0, 0};
-        L::run(acc, o, smem, m0, n0, k_lo, k_hi, wave, lane);
+        L::run(acc, o, (pair::lds_char*)smem_raw + part * L::LDS, m0, n0, k_lo, k_hi, each, wave, lane);
+        __syncthreads();  // (every wave is done with the operands in LDS)
+        f4 mine[FP][4];   // the row tiles from `first` on
+        const int first = part * FP;
+        if constexpr (PARTS == 1) {
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mine[i][j] = acc[i][j];
+        } else {
+            static_assert(PARTS == 2, "");
+            // each part finishes half of the row tiles and hands the others over
+            f4* lds = (f4*)smem_raw;
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mine[i][j] = part ? acc[FP + i][j] : acc[i][j];
+                    lds[(id * FP * 4 + i * 4 + j) * 64 + lane] = part ? acc[i][j] : acc[FP + i][j];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mine[i][j] += lds[((id ^ L::NW) * FP * 4 + i * 4 + j) * 64 + lane];
+            __syncthreads();
+        }
         if (p.split > 1) {
-            f4* w = (f4*)p.ws + ((int64_t)nidx * L::NW + wave) * FM * 4 * 64 + lane;
+            f4* w = (f4*)p.ws + (((int64_t)nidx * L::NW + wave) * FM + first) * 4 * 64 + lane;
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FP; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[(i * 4 + j) * 64] = acc[i][j];
+                for (int j = 0; j < 4; ++j) w[(i * 4 + j) * 64] = mine[i][j];
             return;
         }
-        __syncthreads();  // (every wave is done with the operands in LDS)
         const bool across = p.E && !(p.symmetric && tm == tn);
 #pragma unroll
-        for (int i = 0; i < FM; i += 2) {
+        for (int i = 0; i < FP; i += 2) {
             f4 two[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) two[0][j] = acc[i][j], two[1][j] = acc[i + 1][j];
-            finish(two, p, entry, m0 + wm * L::TM + 16 * i, n0 + wn * 64, across, (unsigned*)smem_raw + wave * kWaveWords, lane);
+            for (int j = 0; j < 4; ++j) two[0][j] = mine[i][j], two[1][j] = mine[i + 1][j];
+            finish(two, p, entry, m0 + wm * L::TM + 16 * (first + i), n0 + wn * 64, across, (unsigned*)smem_raw + id * kWaveWords, lane);
         }
     }
 
@@ -338,17 +365,25 @@ struct Tile {
         f4 two[2][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j) two[j >> 2][j & 3] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int k = 0; k < p.split; ++k) {
+        for (int k = 0; k < p.split; k += 4) {
+            f4 x[4][8];  // (in flight together)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) two[j >> 2][j & 3] += w[k * step + j * 64];
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (k + u < p.split) x[u][j] = w[(k + u) * step + j * 64];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (k + u < p.split) two[j >> 2][j & 3] += x[u][j];
         }
         finish(two, p, entry, (int64_t)tm * L::BM + wm * L::TM + 16 * i, (int64_t)tn * L::BN + wn * 64, p.E && !(p.symmetric && tm == tn), lds, lane);
     }
 };
 
 template <int CFG>
-__global__ __launch_bounds__((Tile<CFG>::L::NT)) __attribute__((amdgpu_waves_per_eu(2))) void ortho_tile_kernel(OrthoMul p) {
+__global__ __launch_bounds__((Tile<CFG>::NT)) __attribute__((amdgpu_waves_per_eu(2))) void ortho_tile_kernel(OrthoMul p) {
     Tile<CFG>::run(p);
 }
 template <int CFG>
@@ -360,7 +395,7 @@ template <int CFG>
 int launch_mul(const OrthoMul& p, hipStream_t s) {
     using X = Tile<CFG>;
     const int64_t tiles = (int64_t)p.tiles * p.batch;
-    hipLaunchKernelGGL(ortho_tile_kernel<CFG>, dim3((unsigned)(tiles * p.split)), dim3(X::L::NT), 0, s, p);
+    hipLaunchKernelGGL(ortho_tile_kernel<CFG>, dim3((unsigned)(tiles * p.split)), dim3(X::NT), 0, s, p);
     if (p.split > 1) hipLaunchKernelGGL(ortho_sum_kernel<CFG>, dim3((unsigned)(tiles * X::L::NW * X::FM / 2)), dim3(64), 0, s, p);
     return (int)hipGetLastError();
 }

@@ -317,9 +317,10 @@ struct Loop {
         f.st = sn;
     }
 
-    // K-steps [k_lo, k_hi) of tile (m0, n0)
+    // K-steps [k_lo, k_hi) of tile (m0, n0).  (split: `steps` of them, those from k_hi on with zeros, so that the parts of a
+    // workgroup meet at as many barriers)
     __device__ __forceinline__ static void run(f4 (&acc)[FM][4], const Operands& a, lds_char* smem, int64_t m0, int64_t n0, int k_lo,
-                                               int k_hi, int wave, int lane) {
+                                               int k_hi, int steps, int wave, int lane) {
         const int wm = wave / WN, wn = wave % WN;
         Dma d;
         dma_setup(d, a, m0, n0, k_lo, k_hi, wave, lane);
@@ -350,12 +351,16 @@ struct Loop {
         read_rows(f.fr[0], smem, l, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) read_col(f.fc, smem, l, j);
-        int kt = k_lo;
-        const int plain = k_tail && k_lo < last ? last - 1 : k_hi;
-        for (; kt < plain; ++kt) kstep<false>(acc, f, d, l, smem, 0, wave);
-        if (kt < k_hi) {
-            kstep<true>(acc, f, d, l, smem, k_tail, wave);
-            kstep<false>(acc, f, d, l, smem, 0, wave);
+        if constexpr (FP4) {
+            int kt = k_lo;
+            const int plain = k_tail && k_lo < last ? last - 1 : k_hi;
+            for (; kt < plain; ++kt) kstep<false>(acc, f, d, l, smem, 0, wave);
+            if (kt < k_hi) {
+                kstep<true>(acc, f, d, l, smem, k_tail, wave);
+                kstep<false>(acc, f, d, l, smem, 0, wave);
+            }
+        } else {
+            for (int i = 0; i < steps; ++i) kstep<false>(acc, f, d, l, smem, 0, wave);
         }
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // (nothing lands in LDS after the workgroup)
     }

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 
 #include "api_util.h"
 #include "lowp.h"
@@ -183,13 +184,20 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
     };
     const auto plan = [&](int64_t M, int64_t N, int64_t K, int64_t entries, bool sym) {
         Plan best{};
+        double best_t = 1e30;
         for (int c = 0; c < kNumOrthoTiles; ++c) {
             const OrthoTile& x = kOrthoTiles[c];
             const int64_t tm = (M + x.bm - 1) / x.bm, tn = (N + x.bn - 1) / x.bn, tiles = sym ? tm * (tm + 1) / 2 : tm * tn;
-            const int64_t slots = 256 * x.per_cu, all = tiles * entries, ksteps = pad(K) / 32;
-            const int64_t split = std::max<int64_t>(1, std::min({slots / all, ksteps / 4, (int64_t)16}));
-            best = Plan{c, (int)tm, (int)tn, (int)tiles, (int)split, split > 1 ? all * split * x.bm * x.bn * 4 : 0};
-            if (all >= 192) break;
+            const int64_t all = tiles * entries, ksteps = pad(K) / 32;
+            for (int64_t s = 1; s <= std::min<int64_t>(ksteps, 32); ++s) {
+                if (getenv("OC") && (atoi(getenv("OC")) != c)) continue;
+                const char* e = sym ? (K == M ? getenv("OT") : getenv("OS")) : getenv("OX");
+                if (e && atoi(e) != s) continue;
+                static constexpr double kStep[2] = {1.6, 0.5}, kRound[2] = {6, 4};
+                const int64_t rounds = (all * s + 255) / 256;
+                const double time = rounds * (kRound[c] + kStep[c] * ((ksteps + s - 1) / s)) + (s > 1 ? 4 + 2.0 * all * s * x.bm * x.bn * 4 / 4e6 : 0);
+                if (time < best_t) best_t = time, best = Plan{c, (int)tm, (int)tn, (int)tiles, (int)s, s > 1 ? all * s * x.bm * x.bn * 4 : 0};
+            }
         }
         return best;
     };
