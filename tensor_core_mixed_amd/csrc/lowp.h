@@ -215,10 +215,11 @@ int launch_fp4_skinny(int rows, const Fp4Args& a, void* stream);
 struct OrthoTile {
     int bm, bn, wm, wn, stages, parts;
 };
-constexpr int kNumOrthoTiles = 2;
+constexpr int kNumOrthoTiles = 3;
 constexpr OrthoTile kOrthoTiles[kNumOrthoTiles] = {
     {256, 256, 2, 4, 2, 1},  // large products
-    {128, 128, 2, 2, 2, 2},  // their sum over the two halves of k in LDS
+    {128, 128, 2, 2, 2, 2},  // few tiles: two halves of k, added in LDS
+    {64, 64, 2, 1, 2, 4},    // fewer: four quarters
 };
 // sizes up to 2^20 - 32 (a tile's rows stay within a buffer descriptor's range), workspace of the entries of a launch, slices
 // of a sum of squares

@@ -25,7 +25,8 @@
 //         tile column; the others are those transposed,
 //     X = a X + T X, with rows of X transposed as second operand; its
 //         tiles leave as they are and transposed (through LDS, a wave its own
-//         64 x 32 values at a time) for the next step.
+//         64 x 32 values at a time) for the next step.  (a within T, on the
+//         diagonal, would save reading X here and lose bits of a X.)
 //
 // Few tiles leave CUs without work: k is cut into two halves within a
 // workgroup of small tiles (their sum goes through LDS) and into ranges, one a
@@ -112,23 +113,29 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(OrthoArgs a) {
     __shared__ double part[kThreads / 64];
     const int64_t entry = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
     const char* g = (const char*)a.g + entry * a.stride_g * ES;
-    const int64_t per_row = (a.cols + N - 1) / N, total = a.rows * per_row;
+    const unsigned per_row = (unsigned)((a.cols + N - 1) / N);
     double s = 0;
-    for (int64_t i = slice * kThreads + threadIdx.x; i < total; i += a.slices * kThreads) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * N;
-        const char* p = g + (r * a.ldg + c) * ES;
-        if (c + N <= a.cols) {
+    // pieces of N values, in a row's order: this thread's first, and how far it goes on
+    const int64_t first = slice * kThreads + threadIdx.x, hop = a.slices * kThreads;
+    int64_t r = first / per_row, c = first % per_row;
+    const int64_t hop_r = hop / per_row, hop_c = hop % per_row;
+#pragma unroll 2
+    for (; r < a.rows; r += hop_r, c += hop_c) {
+        if (c >= per_row) c -= per_row, ++r;
+        if (r >= a.rows) break;
+        const char* p = g + (r * a.ldg + c * N) * ES;
+        if (c * N + N <= a.cols) {
             unsigned w[N * ES / 4];
             __builtin_memcpy(w, p, N * ES);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const double v = (double)load_float<XT>((const char*)w, j);
-                s += v * v;
+                s = __builtin_fma(v, v, s);
             }
         } else {
-            for (int64_t j = 0; c + j < a.cols; ++j) {
+            for (int64_t j = 0; c * N + j < a.cols; ++j) {
                 const double v = (double)load_float<XT>(p, j);
-                s += v * v;
+                s = __builtin_fma(v, v, s);
             }
         }
     }
@@ -192,7 +199,7 @@ struct Tile {
     using L = pair::Loop<kOrthoTiles[CFG].bm, kOrthoTiles[CFG].bn, kOrthoTiles[CFG].wm, kOrthoTiles[CFG].wn, kOrthoTiles[CFG].stages, false,
                          false>;
     static constexpr int FM = L::FM, PARTS = kOrthoTiles[CFG].parts, NT = L::NT * PARTS, LDS = L::LDS * PARTS;
-    static constexpr int FP = FM / PARTS;  // row tiles that a wave finishes
+    static constexpr int FP = PARTS == 2 ? FM / 2 : FM;  // row tiles that a wave finishes (of four parts only the first does)
     static_assert(FP % 2 == 0 && L::TM % 32 == 0, "a wave's rows in pairs of tiles");
     static constexpr int kPitch = 33, kWaveWords = 64 * kPitch;
 
@@ -304,29 +311,34 @@ struct Tile {
         L::run(acc, o, (pair::lds_char*)smem_raw + part * L::LDS, m0, n0, k_lo, k_hi, each, wave, lane);
         __syncthreads();  // (every wave is done with the operands in LDS)
         f4 mine[FP][4];   // the row tiles from `first` on
-        const int first = part * FP;
-        if constexpr (PARTS == 1) {
+        const int first = PARTS == 2 ? part * FP : 0;
+        if constexpr (PARTS != 2) {
 #pragma unroll
             for (int i = 0; i < FP; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mine[i][j] = acc[i][j];
-        } else {
-            static_assert(PARTS == 2, "");
-            // each part finishes half of the row tiles and hands the others over
+        }
+        if constexpr (PARTS > 1) {
+            // two parts: each finishes half of the row tiles and hands the others over; more: the first finishes all
             f4* lds = (f4*)smem_raw;
 #pragma unroll
             for (int i = 0; i < FP; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    mine[i][j] = part ? acc[FP + i][j] : acc[i][j];
-                    lds[(id * FP * 4 + i * 4 + j) * 64 + lane] = part ? acc[i][j] : acc[FP + i][j];
+                    if constexpr (PARTS == 2) mine[i][j] = part ? acc[FP + i][j] : acc[i][j];
+                    lds[(id * FP * 4 + i * 4 + j) * 64 + lane] = PARTS == 2 && !part ? acc[FM - FP + i][j] : acc[i][j];
                 }
             __syncthreads();
+            if (PARTS == 2 || part == 0) {
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
+                for (int q = 1; q < PARTS; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mine[i][j] += lds[((id ^ L::NW) * FP * 4 + i * 4 + j) * 64 + lane];
+                    for (int i = 0; i < FP; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mine[i][j] += lds[((PARTS == 2 ? id ^ L::NW : q * L::NW + wave) * FP * 4 + i * 4 + j) * 64 + lane];
+            }
             __syncthreads();
+            if (PARTS > 2 && part) return;
         }
         if (p.split > 1) {
             f4* w = (f4*)p.ws + (((int64_t)nidx * L::NW + wave) * FM + first) * 4 * 64 + lane;
@@ -346,10 +358,11 @@ struct Tile {
         }
     }
 
-    // The sum of a split launch: a wave takes two row tiles of one of its waves.
+    // The sum of a split launch: four waves take two row tiles of one of its waves, each adds the ranges of two of the
+    // eight accumulators (many of their reads in flight), and one finishes them.
     __device__ __forceinline__ static void run_sum(const OrthoMul& p) {
-        __shared__ unsigned lds[kWaveWords];
-        const int lane = threadIdx.x;
+        __shared__ __attribute__((aligned(16))) unsigned lds[kWaveWords];
+        const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
         int64_t b = blockIdx.x;
         const int i = (int)(b % (FM / 2)) * 2;
         b /= FM / 2;
@@ -360,24 +373,27 @@ struct Tile {
         int tm, tn;
         tile_at(p, t, &tm, &tn);
         const int wm = wave / L::WN, wn = wave % L::WN;
-        const f4* w = (const f4*)p.ws + (((entry * p.split * p.tiles + t) * L::NW + wave) * FM + i) * 4 * 64 + lane;
+        const f4* w = (const f4*)p.ws + (((entry * p.split * p.tiles + t) * L::NW + wave) * FM + i) * 4 * 64 + 2 * q * 64 + lane;
         const int64_t step = (int64_t)p.tiles * L::NW * FM * 4 * 64;
+        f4 s[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
+        for (int k = 0; k < p.split; k += 8) {
+            f4 x[8][2];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k + u < p.split) x[u][0] = w[(k + u) * step], x[u][1] = w[(k + u) * step + 64];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k + u < p.split) s[0] += x[u][0], s[1] += x[u][1];
+        }
+        f4* l = (f4*)lds;
+        l[(2 * q) * 64 + lane] = s[0];
+        l[(2 * q + 1) * 64 + lane] = s[1];
+        __syncthreads();
+        if (q) return;
         f4 two[2][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) two[j >> 2][j & 3] = f4{0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < p.split; k += 4) {
-            f4 x[4][8];  // (in flight together)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (k + u < p.split) x[u][j] = w[(k + u) * step + j * 64];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (k + u < p.split) two[j >> 2][j & 3] += x[u][j];
-        }
+        for (int j = 0; j < 8; ++j) two[j >> 2][j & 3] = l[j * 64 + lane];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (before finish() writes there)
         finish(two, p, entry, (int64_t)tm * L::BM + wm * L::TM + 16 * i, (int64_t)tn * L::BN + wn * 64, p.E && !(p.symmetric && tm == tn), lds, lane);
     }
 };
@@ -387,7 +403,7 @@ __global__ __launch_bounds__((Tile<CFG>::NT)) __attribute__((amdgpu_waves_per_eu
     Tile<CFG>::run(p);
 }
 template <int CFG>
-__global__ __launch_bounds__(64) void ortho_sum_kernel(OrthoMul p) {
+__global__ __launch_bounds__(256) void ortho_sum_kernel(OrthoMul p) {
     Tile<CFG>::run_sum(p);
 }
 
@@ -396,7 +412,7 @@ int launch_mul(const OrthoMul& p, hipStream_t s) {
     using X = Tile<CFG>;
     const int64_t tiles = (int64_t)p.tiles * p.batch;
     hipLaunchKernelGGL(ortho_tile_kernel<CFG>, dim3((unsigned)(tiles * p.split)), dim3(X::NT), 0, s, p);
-    if (p.split > 1) hipLaunchKernelGGL(ortho_sum_kernel<CFG>, dim3((unsigned)(tiles * X::L::NW * X::FM / 2)), dim3(64), 0, s, p);
+    if (p.split > 1) hipLaunchKernelGGL(ortho_sum_kernel<CFG>, dim3((unsigned)(tiles * X::L::NW * X::FM / 2)), dim3(256), 0, s, p);
     return (int)hipGetLastError();
 }
 
@@ -425,8 +441,9 @@ int launch_ortho_start(int x_type, const OrthoArgs& a, float factor, bool out, v
     }
 }
 int launch_ortho_mul(int cfg, const OrthoMul& p, void* stream) {
-    static_assert(kNumOrthoTiles == 2, "one case a config");
-    return cfg == 0 ? ortho::launch_mul<0>(p, (hipStream_t)stream) : ortho::launch_mul<1>(p, (hipStream_t)stream);
+    static_assert(kNumOrthoTiles == 3, "one case a config");
+    hipStream_t s = (hipStream_t)stream;
+    return cfg == 0 ? ortho::launch_mul<0>(p, s) : (cfg == 1 ? ortho::launch_mul<1>(p, s) : ortho::launch_mul<2>(p, s));
 }
 
 }  // namespace tcm

@@ -61,12 +61,13 @@ struct Loop {
     static_assert(BN / WN == 64, "a wave covers 64 columns");
     static constexpr int GM = FM >= 4 ? 2 : 1, NG = FM / GM;  // row tiles taken together, groups a K-step
     static_assert(FM % (2 * GM) == 0, "a step starts with the first of the two fragment buffers");
-    static_assert(NW == 8 || NW == 4, "");
+    static_assert(NW == 8 || NW == 4 || (NW == 2 && !FP4), "");
+    static constexpr int NB = NW == 8 ? 1 : 8 / NW;  // offsets of B's copies: the swizzle of rows 8 NW apart differs
     static constexpr int IA = BM / (8 * NW), IB = BN / (8 * NW);
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + NW * 256;
     static constexpr int STAGE = FP4 ? SB_OFF + NW * 256 : SA_OFF;
     static constexpr int LDS = NST * STAGE;
-    static_assert(LDS <= 160 * 1024 && 2 * BM <= 64 * NW && 2 * BN <= 64 * NW, "a wave copies 64 scale words of each operand");
+    static_assert(LDS <= 160 * 1024 && (!FP4 || (2 * BM <= 64 * NW && 2 * BN <= 64 * NW)), "a wave copies 64 scale words of each operand");
 
     // The column of the wave's 64 that is row i of its tile j, and its parts: n_row(i) + n_tile(j).
     __device__ __forceinline__ static constexpr int n_row(int i) { return WIDE ? i : 16 * (i >> 2) + (i & 3); }
@@ -82,8 +83,8 @@ struct Loop {
     // A wave's copies of a step: IA of A, IB of B, and one of each operand's scales.
     static constexpr int NS = FP4 ? 2 : 0, OPS = IA + IB + NS;
     struct Dma {
-        unsigned a_off, b_off[2], s_off[2];
-        int a_k, b_k[2], s_k[2];
+        unsigned a_off, b_off[NB], s_off[2];
+        int a_k, b_k[NB], s_k[2];
         const unsigned char *pa, *pb;
         const unsigned* ps[2];
         int64_t s_step[2];  // words
@@ -92,7 +93,7 @@ struct Loop {
         int a_range, b_range, k_left, steps_left;
         // of the step being copied: offsets, out of range past its data, and ranges, empty past the last step.  (The
         // range is checked against the lane's offset alone, so the whole of it goes there.)
-        unsigned oa, ob[2], os[2];
+        unsigned oa, ob[NB], os[2];
         int ra, rb;
     };
     __device__ __forceinline__ static void dma_setup(Dma& d, const Operands& a, int64_t m0, int64_t n0, int k_lo, int k_hi, int wave,
@@ -103,7 +104,7 @@ struct Loop {
             d.a_k = 16 * c;
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // (with four waves the swizzle of rows 32 apart differs: two offsets)
+        for (int q = 0; q < NB; ++q) {
             const int r = 8 * (NW * q + wave) + (lane >> 3), c = chunk((lane & 7) ^ swz_b(r));
             d.b_off[q] = (unsigned)(r * (int)a.ldb + 16 * c);
             d.b_k[q] = 16 * c;
@@ -125,7 +126,7 @@ struct Loop {
         d.pa = a.A + m0 * a.lda + k0;
         d.pb = a.B + n0 * a.ldb + k0;
         d.a_hop = (unsigned)(8 * NW * (int)a.lda);
-        d.b_hop = (unsigned)(16 * NW * (int)a.ldb);
+        d.b_hop = (unsigned)(8 * NW * NB * (int)a.ldb);
         // the ranges end with the last row's last 16-byte chunk (which may hold values past K)
         const int left = (int)(a.row_bytes - k0);
         const int rows_a = (int)min<int64_t>(a.M - m0, BM), rows_b = (int)min<int64_t>(a.N - n0, BN);
@@ -145,8 +146,8 @@ struct Loop {
             d.ra = left > 0 ? d.a_range : 0;
             d.rb = left > 0 ? d.b_range : 0;
             d.oa = d.a_k < left ? d.a_off : kOOB;
-            d.ob[0] = d.b_k[0] < left ? d.b_off[0] : kOOB;
-            d.ob[1] = d.b_k[1] < left ? d.b_off[1] : kOOB;
+#pragma unroll
+            for (int q = 0; q < NB; ++q) d.ob[q] = d.b_k[q] < left ? d.b_off[q] : kOOB;
 #pragma unroll
             for (int q = 0; q < NS; ++q) d.os[q] = d.s_k[q] < left ? d.s_off[q] : kOOB;
         }
@@ -156,7 +157,7 @@ struct Loop {
         } else if (op < IA + IB) {
             const int j = op - IA;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.pb, d.rb), (lds_void*)(s + A_BYTES + (NW * j + wave) * 1024), 16,
-                                                     d.ob[j & 1] + (j >> 1) * d.b_hop, 0, 0, 0);
+                                                     d.ob[j % NB] + (j / NB) * d.b_hop, 0, 0, 0);
         } else {
             const int q = op - IA - IB;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(d.ps[q], (int)kOOB), (lds_void*)(s + d.s_lds[q]), 4, d.os[q], 0, 0, 0);

@@ -193,7 +193,7 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
                 if (getenv("OC") && (atoi(getenv("OC")) != c)) continue;
                 const char* e = sym ? (K == M ? getenv("OT") : getenv("OS")) : getenv("OX");
                 if (e && atoi(e) != s) continue;
-                static constexpr double kStep[2] = {1.6, 0.5}, kRound[2] = {6, 4};
+                static constexpr double kStep[3] = {1.6, 0.7, 0.2}, kRound[3] = {10, 10, 8};
                 const int64_t rounds = (all * s + 255) / 256;
                 const double time = rounds * (kRound[c] + kStep[c] * ((ksteps + s - 1) / s)) + (s > 1 ? 4 + 2.0 * all * s * x.bm * x.bn * 4 / 4e6 : 0);
                 if (time < best_t) best_t = time, best = Plan{c, (int)tm, (int)tn, (int)tiles, (int)s, s > 1 ? all * s * x.bm * x.bn * 4 : 0};
