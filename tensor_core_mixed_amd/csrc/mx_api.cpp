@@ -102,7 +102,8 @@ bool fp4_tiles_fit(const Fp4Args& a) {
 // pipelines and its K-steps, whose time grows from `lone` to `shared` as the
 // chip fills, or the operands' way from memory where that is longer; C's or
 // the partial tiles' way out; and for a split the sum's launch, each share's
-// part of it and the partial tiles' way back.
+// part of it and the partial tiles' way back.  Fitted to products of 1 to 8192
+// rows.
 struct Fp4Plan {
     int config, split;
 };
@@ -110,7 +111,7 @@ Fp4Plan plan_fp4(const Fp4Args& a, const LowpOpts& o) {
     static constexpr struct {
         int per_cu;
         double lone, shared;
-    } kStep[kNumFp4Tiles] = {{1, 1.28, 1.65}, {1, 0.66, 0.93}, {2, 0.69, 1.04}, {2, 0.38, 0.63}};
+    } kStep[kNumFp4Tiles] = {{1, 1.28, 1.68}, {1, 0.7, 1.03}, {2, 0.6, 1.2}, {2, 0.31, 0.72}};
     // a launch counts its threads in 32 bits: so many workgroups of a product, at most 512 threads each, and of a sum, 256
     // threads for 1024 outputs
     constexpr int64_t kMaxWgs = (int64_t)1 << 22, kMaxSums = ((int64_t)1 << 24) - 1;
@@ -142,7 +143,7 @@ Fp4Plan plan_fp4(const Fp4Args& a, const LowpOpts& o) {
     }
     // Few rows: a workgroup's waves take a step each at a time, rows cost reads of A from the caches.
     if (forced < 0 ? a.M <= kFp4SkinnyRows : forced == kFp4Skinny) {
-        static constexpr double kBlock[4] = {0.87, 1.4, 1.75, 2.6};
+        static constexpr double kBlock[4] = {1.0, 1.3, 1.9, 2.0}, kFixedFew = 4.5, kSumFew = 4;
         const int64_t blocks_m = (a.M + kFp4SkinnyRows - 1) / kFp4SkinnyRows;
         const int64_t wgs = blocks_m * ((a.N + kFp4SkinnyCols - 1) / kFp4SkinnyCols);
         const double round = kBlock[std::min<int64_t>((a.M + blocks_m * 16 - 1) / (blocks_m * 16), 4) - 1];
@@ -150,8 +151,8 @@ Fp4Plan plan_fp4(const Fp4Args& a, const LowpOpts& o) {
         const int64_t most = std::min({(int64_t)kFp4MaxSplit, steps, (kMaxWgs - 1) / wgs});
         for (int s = 1; s <= most; ++s) {
             if (o.fp4_split && s != std::min<int64_t>(o.fp4_split, most)) continue;
-            const double time = kFixed + std::max((double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round, memory) +
-                                (s > 1 ? kSum + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
+            const double time = kFixedFew + std::max((double)((wgs * s + 255) / 256) * (double)((steps + 8 * s - 1) / (8 * s)) * round, memory) +
+                                (s > 1 ? kSumFew + kShare * s + 8.0 * s * (double)a.M * (double)a.N / kBytesPerUs : 0);
             if (time < best_t || forced == kFp4Skinny && best.config != kFp4Skinny) best_t = time, best = {kFp4Skinny, s};
         }
     }

@@ -163,7 +163,6 @@ __global__ __launch_bounds__(kThreads) void start_kernel(OrthoArgs a, float fact
     const int64_t b = a.first_tile + blockIdx.x, entry = b / tiles, t = b % tiles;
     const int64_t r0 = t / tc * 64, c0 = t % tc * 64;
     const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
-    const double f = inverse_norm(a, entry) * (double)factor;
     const char* g = (const char*)a.g + (entry * a.stride_g + (r0 + r) * a.ldg + c0 + c) * ES;
     float v[16];
     const int64_t n = r0 + r < a.rows ? a.cols - c0 - c : 0;
@@ -176,6 +175,7 @@ __global__ __launch_bounds__(kThreads) void start_kernel(OrthoArgs a, float fact
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = j < n ? load_float<XT>(g, j) : 0.f;
     }
+    const double f = inverse_norm(a, entry) * (double)factor;
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = j < n ? (float)((double)v[j] * f) : 0.f;  // (zeros past the matrix, also under a NaN norm)
     if constexpr (OUT) {

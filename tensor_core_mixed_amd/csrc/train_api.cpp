@@ -5,7 +5,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
-#include <cstdlib>
 
 #include "api_util.h"
 #include "lowp.h"
@@ -177,26 +176,30 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
     // an entry's parts: X, X transposed twice (read by other tiles while the next is written), S, T
     const int64_t x_bytes = line(n * pad(m) * 4), xt_bytes = line(m * pad(n) * 4), s_bytes = line(n * pad(n) * 4);
     const int64_t entry = steps ? x_bytes + 2 * xt_bytes + 2 * s_bytes : 0;
-    // The tile and the k ranges of a product, by the workgroups that the chip holds at once.
+    // The tile and the k ranges of a product by a model of its time, in microseconds: the launch; for every round of
+    // workgroups a fill and the tiles' way out, and its K-steps; for ranges the second launch and the partial tiles' way
+    // there and back.  Fitted to products of 768 to 4096 rows.
     struct Plan {
         int cfg, tiles_m, tiles_n, tiles, split;
         int64_t ws;
     };
     const auto plan = [&](int64_t M, int64_t N, int64_t K, int64_t entries, bool sym) {
+        static constexpr struct {
+            double whole, part, step;
+        } kRound[kNumOrthoTiles] = {{12, 8, 2.5}, {12, 6.5, 0.65}, {5, 5, 0.27}};
+        constexpr double kLaunch = 3, kSum = 5, kBytesPerUs = 3e6;
+        constexpr int64_t kMaxSplit = 32;
         Plan best{};
         double best_t = 1e30;
         for (int c = 0; c < kNumOrthoTiles; ++c) {
             const OrthoTile& x = kOrthoTiles[c];
             const int64_t tm = (M + x.bm - 1) / x.bm, tn = (N + x.bn - 1) / x.bn, tiles = sym ? tm * (tm + 1) / 2 : tm * tn;
             const int64_t all = tiles * entries, ksteps = pad(K) / 32;
-            for (int64_t s = 1; s <= std::min<int64_t>(ksteps, 32); ++s) {
-                if (getenv("OC") && (atoi(getenv("OC")) != c)) continue;
-                const char* e = sym ? (K == M ? getenv("OT") : getenv("OS")) : getenv("OX");
-                if (e && atoi(e) != s) continue;
-                static constexpr double kStep[3] = {1.6, 0.7, 0.2}, kRound[3] = {10, 10, 8};
-                const int64_t rounds = (all * s + 255) / 256;
-                const double time = rounds * (kRound[c] + kStep[c] * ((ksteps + s - 1) / s)) + (s > 1 ? 4 + 2.0 * all * s * x.bm * x.bn * 4 / 4e6 : 0);
-                if (time < best_t) best_t = time, best = Plan{c, (int)tm, (int)tn, (int)tiles, (int)s, s > 1 ? all * s * x.bm * x.bn * 4 : 0};
+            for (int64_t s = 1; s <= std::min(ksteps, kMaxSplit); ++s) {
+                const double rounds = (double)((all * s + 255) / 256), bytes = (double)(all * s * x.bm * x.bn * 4);
+                const double time = kLaunch + rounds * ((s > 1 ? kRound[c].part : kRound[c].whole) + kRound[c].step * (double)((ksteps + s - 1) / s)) +
+                                    (s > 1 ? kSum + bytes / kBytesPerUs : 0);
+                if (time < best_t) best_t = time, best = Plan{c, (int)tm, (int)tn, (int)tiles, (int)s, s > 1 ? (int64_t)bytes : 0};
             }
         }
         return best;
