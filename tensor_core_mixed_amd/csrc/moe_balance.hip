@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
 #pragma unroll
             for (int i = 0; i < NPL; ++i) x[i] = 0.f;
         }
-        const bool live = scores<LPT, NPL, Y, SIG>(e, p, r, &at, x, far, a.experts, sub) && on;
+        const bool live = scores<LPT, NPL, Y, SIG>(e, p, r, &at, x, far, a.experts, sub) && on && a.experts > 0;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) sum += e[i];
@@ -335,12 +335,12 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
 }
 
 // The partial sums of 16 experts a workgroup (of 64: 8.4 us of 16384 x 256's, five of them reading on four CUs).  Their
-// parts of sum n p / (T k T), which lies in [0, 1], are added as integers of 2^-40 in the word that also counts the
+// parts of sum n p / (T k T), which lies in [0, 1], are added as integers of 2^-49 in the word that also counts the
 // arrivals (and those with a NaN): one atomic addition hands everything on, without a fence, and gives the same sum in
-// any order.  (Loss: off by experts * 2^-41 * experts / 16 at most, about half a step of binary32 near 1.)
+// any order.  (The loss is off by experts^2 / 16 * 2^-50 at most, 2^-34 for 1024 of them.)
 constexpr int kJoinWaves = 16, kJoinExperts = 16, kJoinSlices = kJoinWaves * 4, kJoinRows = (kBalanceGroups + kJoinSlices - 1) / kJoinSlices;
-constexpr int kFraction = 40, kNans = 48, kArrivals = 56;
-static_assert((kRouteMaxExperts + kJoinExperts - 1) / kJoinExperts <= 128, "counts of arrivals in 8 bits");
+constexpr int kFraction = 49, kNans = 50, kArrivals = 57;
+static_assert((kRouteMaxExperts + kJoinExperts - 1) / kJoinExperts < 128, "counts of arrivals in 7 bits");
 __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(BalanceArgs a) {
     __shared__ double sp[kJoinWaves][kJoinExperts], sz[kBalanceGroups / 64];
     __shared__ int sn[kJoinWaves][kJoinExperts], sv[kBalanceGroups / 64];
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(BalanceAr
     const uint64_t mine = part == part ? (uint64_t)(part * (double)(1ull << kFraction) + 0.5) : 1ull << kNans;
     const uint64_t sum = mine + __hip_atomic_fetch_add(a.arrived, mine + (1ull << kArrivals), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if ((sum >> kArrivals) != gridDim.x - 1) return;
-    const bool nan = (sum >> kNans) & 255;
+    const bool nan = (sum >> kNans) & 127;
     a.counts[a.experts] = valid;
     a.losses[0] = nan ? __builtin_nanf("") : (float)((double)a.experts * ((double)(sum & ((1ull << kNans) - 1)) / (double)(1ull << kFraction)));
     a.losses[1] = (float)(z / t);
