@@ -218,8 +218,8 @@ struct OrthoTile {
 constexpr int kNumOrthoTiles = 3;
 constexpr OrthoTile kOrthoTiles[kNumOrthoTiles] = {
     {256, 256, 2, 4, 2, 1},  // large products
-    {128, 128, 2, 2, 2, 2},  // few tiles: two halves of k, added in LDS
-    {64, 64, 2, 1, 2, 4},    // fewer: four quarters
+    {128, 128, 4, 2, 3, 1},  // few tiles
+    {64, 64, 2, 1, 3, 2},    // fewer: two halves of k, added in LDS
 };
 // sizes up to 2^20 - 32 (a tile's rows stay within a buffer descriptor's range), workspace of the entries of a launch, slices
 // of a sum of squares

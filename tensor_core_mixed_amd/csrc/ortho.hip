@@ -199,8 +199,7 @@ struct Tile {
     using L = pair::Loop<kOrthoTiles[CFG].bm, kOrthoTiles[CFG].bn, kOrthoTiles[CFG].wm, kOrthoTiles[CFG].wn, kOrthoTiles[CFG].stages, false,
                          false>;
     static constexpr int FM = L::FM, PARTS = kOrthoTiles[CFG].parts, NT = L::NT * PARTS, LDS = L::LDS * PARTS;
-    static constexpr int FP = PARTS == 2 ? FM / 2 : FM;  // row tiles that a wave finishes (of four parts only the first does)
-    static_assert(FP % 2 == 0 && L::TM % 32 == 0, "a wave's rows in pairs of tiles");
+    static_assert(FM % 2 == 0, "a wave's rows in pairs of tiles");
     static constexpr int kPitch = 33, kWaveWords = 64 * kPitch;
 
     // Tile t of an entry's: all of them, or those on and under the diagonal.
@@ -288,7 +287,8 @@ struct Tile {
 
     __device__ __forceinline__ static void run(const OrthoMul& p) {
         __shared__ __attribute__((aligned(1024))) char smem_raw[LDS];
-        static_assert(L::NW * PARTS * kWaveWords * 4 <= LDS && (PARTS == 1 || NT * FP * 4 * 16 <= LDS), "");
+        constexpr int kSums = (PARTS - 1) * L::NT * FM * 16;  // words of the other parts' sums
+        static_assert((kSums + L::NW * kWaveWords) * 4 <= LDS, "");
         const int tid = threadIdx.x, lane = tid & 63;
         const int id = __builtin_amdgcn_readfirstlane(tid >> 6), part = id / L::NW, wave = id % L::NW;
         const int wm = wave / L::WN, wn = wave % L::WN;
@@ -310,51 +310,39 @@ struct Tile {
                                p.k_pad * 4, p.k_pad * 4, p.k_pad * 4, 0, nullptr, nullptr, 0, 0};
         L::run(acc, o, (pair::lds_char*)smem_raw + part * L::LDS, m0, n0, k_lo, k_hi, each, wave, lane);
         __syncthreads();  // (every wave is done with the operands in LDS)
-        f4 mine[FP][4];   // the row tiles from `first` on
-        const int first = PARTS == 2 ? part * FP : 0;
-        if constexpr (PARTS != 2) {
-#pragma unroll
-            for (int i = 0; i < FP; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mine[i][j] = acc[i][j];
-        }
         if constexpr (PARTS > 1) {
-            // two parts: each finishes half of the row tiles and hands the others over; more: the first finishes all
+            // the first part adds the others' sums, in order, and finishes the tile
             f4* lds = (f4*)smem_raw;
+            if (part) {
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
+                for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (PARTS == 2) mine[i][j] = part ? acc[FP + i][j] : acc[i][j];
-                    lds[(id * FP * 4 + i * 4 + j) * 64 + lane] = PARTS == 2 && !part ? acc[FM - FP + i][j] : acc[i][j];
-                }
-            __syncthreads();
-            if (PARTS == 2 || part == 0) {
-#pragma unroll
-                for (int q = 1; q < PARTS; ++q)
-#pragma unroll
-                    for (int i = 0; i < FP; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mine[i][j] += lds[((PARTS == 2 ? id ^ L::NW : q * L::NW + wave) * FP * 4 + i * 4 + j) * 64 + lane];
+                    for (int j = 0; j < 4; ++j) lds[((id - L::NW) * FM * 4 + i * 4 + j) * 64 + lane] = acc[i][j];
             }
             __syncthreads();
-            if (PARTS > 2 && part) return;
+            if (part) return;
+#pragma unroll
+            for (int q = 0; q < PARTS - 1; ++q)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] += lds[((q * L::NW + wave) * FM * 4 + i * 4 + j) * 64 + lane];
         }
         if (p.split > 1) {
-            f4* w = (f4*)p.ws + (((int64_t)nidx * L::NW + wave) * FM + first) * 4 * 64 + lane;
+            f4* w = (f4*)p.ws + ((int64_t)nidx * L::NW + wave) * FM * 4 * 64 + lane;
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[(i * 4 + j) * 64] = mine[i][j];
+                for (int j = 0; j < 4; ++j) w[(i * 4 + j) * 64] = acc[i][j];
             return;
         }
         const bool across = p.E && !(p.symmetric && tm == tn);
 #pragma unroll
-        for (int i = 0; i < FP; i += 2) {
+        for (int i = 0; i < FM; i += 2) {
             f4 two[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) two[0][j] = mine[i][j], two[1][j] = mine[i + 1][j];
-            finish(two, p, entry, m0 + wm * L::TM + 16 * (first + i), n0 + wn * 64, across, (unsigned*)smem_raw + id * kWaveWords, lane);
+            for (int j = 0; j < 4; ++j) two[0][j] = acc[i][j], two[1][j] = acc[i + 1][j];
+            finish(two, p, entry, m0 + wm * L::TM + 16 * i, n0 + wn * 64, across, (unsigned*)smem_raw + kSums + wave * kWaveWords, lane);
         }
     }
 

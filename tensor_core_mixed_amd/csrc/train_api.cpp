@@ -186,7 +186,7 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
     const auto plan = [&](int64_t M, int64_t N, int64_t K, int64_t entries, bool sym) {
         static constexpr struct {
             double whole, part, step;
-        } kRound[kNumOrthoTiles] = {{12, 8, 2.5}, {12, 6.5, 0.65}, {5, 5, 0.27}};
+        } kRound[kNumOrthoTiles] = {{12, 8, 1.65}, {10, 6.5, 0.55}, {5, 5, 0.25}};
         constexpr double kLaunch = 3, kSum = 5, kBytesPerUs = 3e6;
         constexpr int64_t kMaxSplit = 32;
         Plan best{};
