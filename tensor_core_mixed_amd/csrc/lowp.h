@@ -233,13 +233,14 @@ struct OrthoArgs {
     float eps;
     int64_t rows_pad, cols_pad;  // to whole pieces of 32
     int64_t slices;        // of an entry's sum of squares
-    double* squares;       // [batch][slices]
+    double* squares;       // [batch][slices]; null: the launch sums them itself (launch_ortho_small of one chunk)
     char* as_is;           // parts of G over its norm [rows][cols_pad], entry_bytes apart
     char* across;          // and transposed [cols][rows_pad]
     int64_t entry_bytes;
     int64_t first_tile;    // of a launch
 };
-// G's norm, then factor * G / (norm + eps): its parts, or with `out` O
+int launch_ortho_norm(int x_type, const OrthoArgs& a, void* stream);
+// factor * G / (norm + eps): its parts, or with `out` O
 int launch_ortho_start(int x_type, const OrthoArgs& a, float factor, bool out, void* stream);
 
 // alpha * A B^T + beta * P of every entry, in parts: A [M][k_pad], B [N][k_pad], P and D [M][n_pad], E [N][m_pad]
@@ -257,6 +258,32 @@ struct OrthoMul {
     float* ws;             // partial tiles
 };
 int launch_ortho_mul(int cfg, const OrthoMul& p, void* stream);
+
+// Shorter sides up to 128: chunks of kOrthoSmallElems values of an entry's X (64 or 128 rows of it), a workgroup each.
+constexpr int kOrthoSmallMax = 128, kOrthoSmallElems = 16384, kOrthoSmallSteps = 16;
+inline int ortho_small_rows(int64_t n) { return n <= 64 ? 64 : 128; }
+// Every workgroup of an entry reads all its chunks' shares of S: up to half a MiB of them (64 x 8192: 88 us, 126 by
+// ortho.hip's kernels; 128 x 1024: 112, 117).  Of 128 rows they are 64 KiB a chunk, which pays in one round of workgroups
+// only (16 of 128 x 1024: 150, 174; 300 of 100 x 1000: 1800, 1153).
+inline bool ortho_small_fits(int64_t batch, int64_t n, int64_t m) {
+    const int64_t np = ortho_small_rows(n), cw = kOrthoSmallElems / np, chunks = (m + cw - 1) / cw;
+    return n <= kOrthoSmallMax && chunks * np * np * 4 <= (1 << 19) && (np == 64 || chunks == 1 || batch * chunks <= 256);
+}
+struct OrthoStep {
+    float s_alpha, t_alpha, t_beta, x_alpha, x_beta;  // S's factor, and those of T and X as OrthoMul's
+};
+struct OrthoSmallArgs {
+    OrthoArgs g;               // G, O and the norm
+    int64_t m;                 // the longer side
+    int n, tall, chunks;
+    int first, last, steps;    // G becomes X first; O comes out last; steps in between
+    float factor;              // of the first X
+    char* state;               // the chunks' X between launches
+    const float* shares_in;    // the chunks' S of the launch before
+    float* shares_out;
+    OrthoStep step[kOrthoSmallSteps];
+};
+int launch_ortho_small(int x_type, const OrthoSmallArgs& p, void* stream);
 
 // Process-wide switches of tcm_gemm_fp8 (tcm_set_option): the kernel, -1 the
 // planner's choice, else a row of kFp8Tiles, kFp8Skinny or kFp8Generic; and

@@ -7,9 +7,9 @@
 //
 // Every matrix is held in two binary16 parts, value * 2^e = upper + lower: 22
 // bits, of which products keep all but lower times lower (2^-22).  Over five
-// steps that is as exact as binary32 throughout (3.2e-6 against 3.0e-6 of a
-// 768 x 2048 update, from 64 bits; one binary16 part 1.4e-3, two bfloat16
-// ones 2.6e-5), in three matrix instructions of sixteen times binary32's
+// steps that is as exact as binary32 throughout (2.0e-6 against 3.0e-6 of a
+// 768 x 2048 update, from 64 bits; one binary16 part would give 1.4e-3, two
+// bfloat16 ones 2.6e-5), in three matrix instructions of sixteen times binary32's
 // rate.  The exponents e come from bounds: singular values of X lie below 1
 // at first, then below the largest |a s + b s^3 + c s^5| there, and entries
 // below singular values; so nothing passes binary16's range whatever G and
@@ -29,13 +29,23 @@
 //         diagonal, would save reading X here and lose bits of a X.)
 //
 // Few tiles leave CUs without work: k is cut into two halves within a
-// workgroup of small tiles (their sum goes through LDS) and into ranges, one a
-// workgroup, and a second launch adds the partial tiles in order and finishes
-// them.
+// workgroup of the smallest tiles (their sum goes through LDS) and into
+// ranges, one a workgroup, and a second launch adds the partial tiles in order
+// and finishes them.
+//
+// Five steps of 4096 x 1024 take 357 us: 15 products of 209 TFLOP in parts
+// that binary16's library rate would do in 143, the rest being the launches'
+// fill, the way out of 48 MB of X a step and copies that arrive late (of X's
+// product the loop is half).  Eight 768 x 2048: 660 us; 4096 x 4096: 3.7 ms,
+// 65% of that rate.  128 x 128 tiles by eight waves with copies two steps
+// ahead: X's product of 4096 x 1024 27 us, by two groups of four waves, one
+// step ahead, 36; 64 x 64 by two parts two steps ahead 512 x 512 154 us, by
+// four parts one step ahead 170.  Shorter sides up to 128: ortho_small.hip.
 #include <hip/hip_runtime.h>
 
 #include "fp8_util.h"
 #include "lowp.h"
+#include "ortho_util.h"
 #include "pair_tile.h"
 
 namespace tcm {
@@ -43,15 +53,7 @@ namespace ortho {
 
 using pair::f4;
 typedef unsigned u4_t __attribute__((ext_vector_type(4)));
-typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 
-// a value's two parts, the upper in the lower half of the word
-__device__ __forceinline__ unsigned split(float v) {
-    const _Float16 hi = (_Float16)v, lo = (_Float16)(v - (float)hi);
-    return __builtin_bit_cast(unsigned, h2_t{hi, lo});
-}
-__device__ __forceinline__ unsigned upper2(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-__device__ __forceinline__ unsigned lower2(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 // N consecutive values' parts (N a multiple of 8) at column c, a multiple of N, of the row at p
 template <int N>
 __device__ __forceinline__ void store_parts(char* row, int64_t c, const unsigned (&w)[N]) {
@@ -143,14 +145,6 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(OrthoArgs a) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
     __syncthreads();
     if (threadIdx.x == 0) a.squares[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
-}
-
-// 1 / (|G| + eps) of an entry, the same in every thread
-__device__ __forceinline__ double inverse_norm(const OrthoArgs& a, int64_t entry) {
-    double s = 0;
-    for (int i = threadIdx.x & 63; i < a.slices; i += 64) s += a.squares[entry * a.slices + i];
-    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-    return 1 / (sqrt(s) + (double)a.eps);
 }
 
 // G times its inverse norm and `factor`: its parts, as it lies and transposed (64 x 64 values a workgroup), or with
@@ -405,8 +399,12 @@ int launch_mul(const OrthoMul& p, hipStream_t s) {
 }
 
 template <int XT>
-int launch_start(const OrthoArgs& a, float factor, bool out, hipStream_t s) {
+int launch_norm(const OrthoArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(norm_kernel<XT>, dim3((unsigned)(a.batch * a.slices)), dim3(kThreads), 0, s, a);
+    return (int)hipGetLastError();
+}
+template <int XT>
+int launch_start(const OrthoArgs& a, float factor, bool out, hipStream_t s) {
     const int64_t tiles = a.batch * ((a.cols_pad + 63) / 64) * ((a.rows_pad + 63) / 64), most = (int64_t)1 << 23;  // (threads: 32 bits)
     for (int64_t t = 0; t < tiles; t += most) {
         OrthoArgs e = a;
@@ -420,6 +418,14 @@ int launch_start(const OrthoArgs& a, float factor, bool out, hipStream_t s) {
 
 }  // namespace ortho
 
+int launch_ortho_norm(int x_type, const OrthoArgs& a, void* stream) {
+    hipStream_t s = (hipStream_t)stream;
+    switch (x_type) {
+    case F16: return ortho::launch_norm<F16>(a, s);
+    case BF16: return ortho::launch_norm<BF16>(a, s);
+    default: return ortho::launch_norm<F32>(a, s);
+    }
+}
 int launch_ortho_start(int x_type, const OrthoArgs& a, float factor, bool out, void* stream) {
     hipStream_t s = (hipStream_t)stream;
     switch (x_type) {

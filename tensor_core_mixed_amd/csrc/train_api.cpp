@@ -145,6 +145,75 @@ int exponent_for(double most) {
     return 13 - std::ilogb(most);
 }
 
+// The factors of step k and of the exponents: `most` bounds X's singular values, `ex` is X's exponent.
+struct OrthoScale {
+    double most = 1.001;  // (the norm bounds them)
+    int ex = exponent_for(1.001);
+    OrthoStep next(const float* coef, bool end, float scale) {
+        const double ca = coef[0], cb = coef[1], cc = coef[2];
+        const auto two = [](double v, int e) { return (float)std::ldexp(v, e); };
+        const int es = exponent_for(most * most), et = exponent_for(largest_square(cb, cc, most * most) * 1.001);
+        most = largest_step(ca, cb, cc, most) * 1.001;
+        const int to = end ? 0 : exponent_for(most);
+        const double f = end ? (double)scale : 1.0;
+        const OrthoStep q{two(1, es - 2 * ex), two(cc, et - 2 * es), two(cb, et - es), two(f, to - et - ex), two(f * ca, to - ex)};
+        ex = to;
+        return q;
+    }
+};
+
+// Shorter sides up to 128 (ortho_small.hip)
+int ortho_small(OrthoArgs a, int x_type, int64_t batch, int steps, const float* coef, float scale, void* stream) {
+    const auto line = [](int64_t x) { return (x + 255) / 256 * 256; };
+    const int64_t n = std::min(a.rows, a.cols), m = std::max(a.rows, a.cols), np = ortho_small_rows(n), cw = kOrthoSmallElems / np;
+    const int64_t chunks = (m + cw - 1) / cw;
+    const bool one = chunks == 1, kept = !one || steps > kOrthoSmallSteps;
+    a.slices = one ? 0 : std::min<int64_t>(kOrthoSlices, (a.rows * ((a.cols + 7) / 8) + 1023) / 1024);
+    const int64_t state = kept ? chunks * kOrthoSmallElems * 4 : 0, shares = kept ? chunks * np * np * 4 : 0, entry = a.slices * 8 + state + 2 * shares;
+    const int64_t part = std::min({batch, std::max<int64_t>(1, kOrthoWorkspace / std::max<int64_t>(entry, 1)), ((int64_t)1 << 22) / chunks});
+    void* ws = nullptr;
+    std::unique_lock<std::mutex> order;
+    if (kept) {
+        const int st = workspace_for(stream, part * (state + 2 * shares) + line(part * a.slices * 8), &ws, &order);
+        if (st != TCM_OK) return st;
+    }
+    set_last_plan(
+        [](char* buf, size_t len, const int64_t* v) {
+            snprintf(buf, len, "kernel=ortho_small batch=%lld rows=%lld cols=%lld dtype=%d steps=%d chunk=%lld chunks=%lld", (long long)v[0],
+                     (long long)v[1], (long long)v[2], (int)v[3], (int)v[4], (long long)v[5], (long long)v[6]);
+        },
+        {batch, a.rows, a.cols, x_type, steps, part, chunks});
+    const char *g = (const char*)a.g, *o = (const char*)a.o;
+    for (int64_t b = 0; b < batch; b += part) {
+        OrthoSmallArgs p{};
+        p.g = a;
+        p.g.g = g + b * a.stride_g * elem_bytes(x_type);
+        p.g.o = (void*)(o + b * a.stride_o * c_elem_bytes(a.o_type));
+        p.g.batch = std::min(part, batch - b);
+        p.m = m;
+        p.n = (int)n;
+        p.tall = a.rows > a.cols;
+        p.chunks = (int)chunks;
+        p.state = (char*)ws;
+        float* s[2] = {(float*)((char*)ws + part * state), (float*)((char*)ws + part * (state + shares))};
+        p.g.squares = one ? nullptr : (double*)((char*)ws + part * (state + 2 * shares));
+        OrthoScale f;
+        p.factor = (float)std::ldexp(1.0, f.ex);
+        if (!one && launch_ortho_norm(x_type, p.g, stream) != 0) return TCM_ERR_HIP;
+        const int each = one ? kOrthoSmallSteps : 1;
+        for (int k = 0, turn = 0; k < steps; ++turn) {
+            p.first = turn == 0;
+            p.steps = p.first && !one ? 0 : std::min(each, steps - k);
+            for (int i = 0; i < p.steps; ++i, ++k) p.step[i] = f.next(coef + 3 * k, k == steps - 1, scale);
+            p.last = k == steps;
+            p.shares_in = s[~turn & 1];
+            p.shares_out = s[turn & 1];
+            if (launch_ortho_small(x_type, p, stream) != 0) return TCM_ERR_HIP;
+        }
+    }
+    return TCM_OK;
+}
+
 int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t ldg, int64_t stride_g, void* o, int64_t ldo,
                int64_t stride_o, int dtype, int steps, const float* coef, float eps, float scale, void* stream) {
     const int t = dtype & 0xff, flags = dtype & ~0xff;
@@ -171,6 +240,20 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
 
     const bool tall = rows > cols;
     const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
+    OrthoArgs a{};
+    a.rows = rows;
+    a.cols = cols;
+    a.ldg = ldg;
+    a.stride_g = stride_g;
+    a.ldo = ldo;
+    a.stride_o = stride_o;
+    a.o_type = o_type;
+    a.eps = eps;
+    if (steps > 0 && ortho_small_fits(batch, n, m)) {
+        a.g = g;
+        a.o = o;
+        return ortho_small(a, t, batch, steps, coef, scale, stream);
+    }
     const auto pad = [](int64_t x) { return (x + 31) / 32 * 32; };
     const auto line = [](int64_t x) { return (x + 255) / 256 * 256; };
     // an entry's parts: X, X transposed twice (read by other tiles while the next is written), S, T
@@ -225,18 +308,9 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
         const int64_t count = std::min(chunk, batch - b);
         char* base = (char*)ws + squares;
         char *x = base, *xt[2] = {base + x_bytes, base + x_bytes + xt_bytes}, *sq = base + x_bytes + 2 * xt_bytes, *tt = sq + s_bytes;
-        OrthoArgs a{};
         a.g = (const char*)g + b * stride_g * elem_bytes(t);
         a.batch = count;
-        a.rows = rows;
-        a.cols = cols;
-        a.ldg = ldg;
-        a.stride_g = stride_g;
         a.o = (char*)o + b * stride_o * c_elem_bytes(o_type);
-        a.ldo = ldo;
-        a.stride_o = stride_o;
-        a.o_type = o_type;
-        a.eps = eps;
         a.rows_pad = pad(rows);
         a.cols_pad = pad(cols);
         a.slices = slices;
@@ -244,13 +318,12 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
         a.as_is = tall ? xt[0] : x;
         a.across = tall ? x : xt[0];
         a.entry_bytes = entry;
-        double most = 1.001;  // of X's singular values (the norm bounds them)
-        int ex = exponent_for(most);
-        if (launch_ortho_start(t, a, steps ? (float)std::ldexp(1.0, ex) : scale, steps == 0, stream) != 0) return TCM_ERR_HIP;
+        OrthoScale f;
+        if (launch_ortho_norm(t, a, stream) != 0) return TCM_ERR_HIP;
+        if (launch_ortho_start(t, a, steps ? (float)std::ldexp(1.0, f.ex) : scale, steps == 0, stream) != 0) return TCM_ERR_HIP;
         for (int k = 0; k < steps; ++k) {
-            const double ca = coef[3 * k], cb = coef[3 * k + 1], cc = coef[3 * k + 2];
-            const int es = exponent_for(most * most), et = exponent_for(largest_square(cb, cc, most * most) * 1.001);
-            const auto two = [](double v, int e) { return (float)std::ldexp(v, e); };
+            const bool end = k == steps - 1;
+            const OrthoStep step = f.next(coef + 3 * k, end, scale);
             const auto mul = [&](const Plan& p, int64_t M, int64_t N, int64_t K, bool sym) {
                 OrthoMul q{};
                 q.entry_bytes = entry;
@@ -273,26 +346,22 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
             OrthoMul q = mul(ps, n, n, m, true);  // S
             q.A = q.B = x;
             q.D = q.E = sq;
-            q.alpha = two(1, es - 2 * ex);
+            q.alpha = step.s_alpha;
             if (launch_ortho_mul(ps.cfg, q, stream) != 0) return TCM_ERR_HIP;
             q = mul(pt, n, n, n, true);  // T
             q.A = q.B = q.P = sq;
             q.D = q.E = tt;
-            q.alpha = two(cc, et - 2 * es);
-            q.beta = two(cb, et - es);
+            q.alpha = step.t_alpha;
+            q.beta = step.t_beta;
             if (launch_ortho_mul(pt.cfg, q, stream) != 0) return TCM_ERR_HIP;
-            most = largest_step(ca, cb, cc, most) * 1.001;
-            const bool end = k == steps - 1;
-            const int next = end ? 0 : exponent_for(most);
-            const double f = end ? (double)scale : 1.0;
             q = mul(px, n, m, n, false);  // X
             q.A = tt;
             q.B = xt[k & 1];
             q.P = x;
             q.D = x;
             q.E = xt[~k & 1];
-            q.alpha = two(f, next - et - ex);
-            q.beta = two(f * ca, next - ex);
+            q.alpha = step.x_alpha;
+            q.beta = step.x_beta;
             if (end) {
                 q.out = (char*)a.o;
                 q.ld_out = ldo;
@@ -301,7 +370,6 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
                 q.out_across = tall;
             }
             if (launch_ortho_mul(px.cfg, q, stream) != 0) return TCM_ERR_HIP;
-            ex = next;
         }
     }
     return TCM_OK;
