@@ -21,6 +21,12 @@
 // lanes of one wave, so no maximum leaves a wave.  Transposed values pass
 // through LDS to be stored 64 bytes of a column at a time.  Row kernel: row
 // blocks as they lie need no tile; short matrices fill more of the chip.
+//
+// Memory bounds all of them: 8003 x 8192 bf16 to both outputs 64 us from HBM
+// (201 MB, 3.1 TB/s; 48 with x in the caches), back from rows 25 (166 MB) and
+// from columns with odd pitches 37.  16 x 4096: 2.4 us.  A tile of 256 x 256
+// by 1024 threads took 52 us for 48 (binary32 109 for 71), stores aligned row
+// by row for odd pitches 82 for 37.
 #include <hip/hip_runtime.h>
 
 #include "fp8_util.h"
