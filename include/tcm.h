@@ -576,7 +576,8 @@ int tcm_gemm_mxfp4(int64_t M, int64_t N, int64_t K,
  * tcm_moe_route_grad's.  experts <= 1024, topk <= 64 and tokens * topk < 2^31
  * (else TCM_ERR_NOT_SUPPORTED), topk <= experts, tokens < 2^31.  A token whose
  * logits are all -inf adds nothing to the losses; NaN and +inf logits make
- * them NaN.  The same call gives the same bits.  Returns as tcm_gemm; the
+ * them NaN.  losses[0] is held to 2^-34 (it is about 1 where the load is even),
+ * losses[1] relative to itself.  The same call gives the same bits.  Returns as tcm_gemm; the
  * workspace rules are tcm_gemm's (calls of up to 128 tokens use none).
  */
 int tcm_moe_balance(int64_t tokens, int64_t experts, int64_t topk,
@@ -641,7 +642,9 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
  * infinity (with no steps its own value only, and zeros of the others).  Any
  * alignment.  rows and cols up to 2^20 - 32 (else TCM_ERR_NOT_SUPPORTED).
  * Returns as tcm_gemm; the workspace rules are tcm_gemm's (it holds G five
- * times in f32's size, for as many entries as 2 GiB take, one at least).
+ * times in f32's size, for as many entries as 2 GiB take, one at least;
+ * entries with one side up to 64 and the other up to 256, or both up to 128,
+ * use none in calls of up to 16 steps).
  */
 int tcm_orthogonalize(int64_t batch, int64_t rows, int64_t cols,
                       const void* G, int64_t ldg, int64_t stride_g,

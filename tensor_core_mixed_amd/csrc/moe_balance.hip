@@ -338,7 +338,7 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
 
 // The partial sums of 16 experts a workgroup (of 64: 8.4 us of 16384 x 256's, five of them reading on four CUs).  Their
 // parts of sum n p / (T k T), which lies in [0, 1], are added as integers of 2^-49 in the word that also counts the
-// arrivals (and those with a NaN): one atomic addition hands everything on, without a fence, and gives the same sum in
+// arrivals (and those with a NaN, or anything else past 1): one atomic addition hands everything on, without a fence, and gives the same sum in
 // any order.  (The loss is off by experts^2 / 16 * 2^-50 at most, 2^-34 for 1024 of them.)
 constexpr int kJoinWaves = 16, kJoinExperts = 16, kJoinSlices = kJoinWaves * 4, kJoinRows = (kBalanceGroups + kJoinSlices - 1) / kJoinSlices;
 constexpr int kFraction = 49, kNans = 50, kArrivals = 57;
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(BalanceAr
     for (int i = 0; i < kBalanceGroups / 64; ++i) z += sz[i], valid += sv[i];
     if (lane != 0) return;
     const double t = valid > 0 ? valid : 1, k = a.topk > 0 ? a.topk : 1, part = dot / (t * k * t);
-    const uint64_t mine = part == part ? (uint64_t)(part * (double)(1ull << kFraction) + 0.5) : 1ull << kNans;
+    const uint64_t mine = part <= 1.5 ? (uint64_t)(part * (double)(1ull << kFraction) + 0.5) : 1ull << kNans;
     const uint64_t sum = mine + __hip_atomic_fetch_add(a.arrived, mine + (1ull << kArrivals), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if ((sum >> kArrivals) != gridDim.x - 1) return;
     const bool nan = (sum >> kNans) & 127;
