@@ -22,11 +22,12 @@
 // through LDS to be stored 64 bytes of a column at a time.  Row kernel: row
 // blocks as they lie need no tile; short matrices fill more of the chip.
 //
-// Memory bounds all of them: 8003 x 8192 bf16 to both outputs 64 us from HBM
-// (201 MB, 3.1 TB/s; 48 with x in the caches), back from rows 25 (166 MB) and
-// from columns with odd pitches 37.  16 x 4096: 2.4 us.  A tile of 256 x 256
-// by 1024 threads took 52 us for 48 (binary32 109 for 71), stores aligned row
-// by row for odd pitches 82 for 37.
+// Memory bounds all of them: 8003 x 8192 bf16 to both outputs 62 us from HBM
+// (201 MB, 3.2 TB/s; 47 with x in the caches), back from rows 25 (166 MB) and
+// from columns with odd pitches 38, whose 16-byte stores lie across lines.
+// 16 x 4096: 2.4 us.  A tile of 256 x 256 by 1024 threads took 52 us for 48
+// (binary32 109 for 71); for odd pitches stores aligned row by row 82 for 37,
+// workgroups of two or four longer pieces of rows 44.
 #include <hip/hip_runtime.h>
 
 #include "fp8_util.h"
@@ -180,7 +181,8 @@ __global__ __launch_bounds__(kThreads) void mx_tile_kernel(MxQuantArgs a) {
     __shared__ unsigned tr[128 * kPitch];
     __shared__ unsigned te[128];  // the columns' scale words
     const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15, wave = tid >> 6;
-    const int64_t bc = blockIdx.x, br = blockIdx.y;
+    // (tiles side by side on one XCD, whose cache joins their halves of Q's lines: 8192 x 8192 bf16 48.1 us to 45.6)
+    const int64_t bc = xcd_order(blockIdx.x, gridDim.x), br = blockIdx.y;
     const int64_t row0 = br * 128 + 8 * rg, col0 = bc * 128 + 8 * cg;
 
     Eight<XT> v[8];
