@@ -633,7 +633,10 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
  *                rounded to nearest even.  Entries must not overlap each other
  *                (stride_o >= (rows-1)*ldo + cols) or G.
  *   steps, coefficients   3 * steps floats in HOST memory, read during the
- *                call; steps >= 0 (0: O = scale * G / (|G| + eps)).
+ *                call; steps >= 0 (0: O = scale * G / (|G| + eps)).  Where they
+ *                can take a singular value past 2^39 or all of them below 2^-39
+ *                before the last step, or b s + c s^2 past 2^79 or below 2^-79,
+ *                the call is refused (TCM_ERR_NOT_SUPPORTED).
  *   eps          >= 0; above 0 it keeps a matrix of zeros one of zeros.
  * Products run on the matrix cores in two binary16 parts of each value, which
  * keep 22 bits, and add in binary32; scales from the coefficients keep them

@@ -137,12 +137,24 @@ double largest_square(double b, double c, double r) {
     if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < r) most = std::max(most, f(-b / (2 * c)));
     return most;
 }
-// The exponent that takes values up to `most` near 2^14, a quarter of binary16's largest.  (A bound that is not finite,
-// or far outside binary32's middle, has values that are none either.)
+// The exponent that takes values up to `most` near 2^14, a quarter of binary16's largest.  (What steps_fit lets pass lies
+// within these bounds, is zero, or is not finite, as its values are then.)
 int exponent_for(double most) {
-    if (!(most > 0x1p-60)) return 60;
-    if (!(most < 0x1p60)) return -60;
+    if (!(most > 0x1p-80)) return 80;
+    if (!(most < 0x1p80)) return -80;
     return 13 - std::ilogb(most);
+}
+// Whether the bounds on X between the steps (whose square is S's) and on T are such that these exponents hold them.
+bool steps_fit(int steps, const float* coef) {
+    double most = 1.001;
+    const auto in = [](double v, double lo, double hi) { return v == 0 || (v >= lo && v <= hi); };
+    for (int k = 0; k < steps; ++k, coef += 3) {
+        const double t = largest_square(coef[1], coef[2], most * most);
+        most = largest_step(coef[0], coef[1], coef[2], most) * 1.001;
+        if (!std::isfinite(t) || !std::isfinite(most)) return true;
+        if (!in(t, 0x1p-79, 0x1p79) || (k < steps - 1 && !in(most, 0x1p-39, 0x1p39))) return false;
+    }
+    return true;
 }
 
 // The factors of step k and of the exponents: `most` bounds X's singular values, `ex` is X's exponent.
@@ -236,7 +248,7 @@ int ortho_impl(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t
     if (gb < 0 || ob < 0) return TCM_ERR_INVALID_VALUE;
     const Region out[1] = {{o, ob}}, in[1] = {{g, gb}};
     if (!disjoint(out, in)) return TCM_ERR_INVALID_VALUE;
-    if (std::max(rows, cols) > kOrthoMaxSize) return TCM_ERR_NOT_SUPPORTED;
+    if (std::max(rows, cols) > kOrthoMaxSize || !steps_fit(steps, coef)) return TCM_ERR_NOT_SUPPORTED;
 
     const bool tall = rows > cols;
     const int64_t n = std::min(rows, cols), m = std::max(rows, cols);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import tensor_core_mixed_amd as T
-from test_gpu_ortho import MUON, check, run, update
+from test_gpu_ortho import MUON, check, run, steps_of, update
 
 pytestmark = pytest.mark.gpu
 SMALL = [(1, 256), (17, 257), (32, 255), (33, 512), (63, 900), (64, 256), (64, 8192), (65, 65), (65, 128), (96, 129), (127, 384), (128, 128), (128, 1024)]
@@ -56,3 +56,14 @@ def test_sizes_of_values(shape):
     base = run(g, eps=0.0)
     for f in (2.0 ** -100, 2.0 ** 100):
         assert torch.equal(run(f * g, eps=0.0)[0], base[0]) and torch.equal(run(f * g, eps=0.0)[2], base[2])
+
+
+@pytest.mark.parametrize("shape", [(2, 30, 40), (2, 150, 200)])
+@pytest.mark.parametrize("coef", [(2.0 ** 38, 0.0, 0.0, 2.0 ** -38, 0.0, 0.0), (2.0 ** -38, 0.0, 0.0, 2.0 ** 38, 0.0, 0.0), (0.0, 2.0 ** -70, 0.0),
+                                  (1.0, 2.0 ** 60, 0.0), (0.0, 0.0, 2.0 ** -75), (0.0, 0.0, 0.0, 1.0, 1.0, 1.0)])
+def test_coefficients_far_from_1(shape, coef):
+    """To 2^-20 (roundings of 2^-22, none of them amplified in one or two steps), also where the same steps in binary32
+    would leave its range (the fourth power of 2^38)."""
+    g = torch.randn(shape, generator=torch.Generator().manual_seed(6))
+    got, ref = run(g, coef).double(), steps_of(g, coef, 1e-7, 1.0, torch.float64)
+    assert ((got - ref).square().sum((1, 2)).sqrt() <= 2.0 ** -20 * ref.square().sum((1, 2)).sqrt()).all()

@@ -155,3 +155,15 @@ def test_update_without_steps_of_a_large_matrix(tmp_path, rows, cols):
         assert T.tcm_orthogonalize(1, {rows}, {cols}, at(1), {cols}, 0, at(1 << 12), {cols}, 0, T.TCM_F16_F32, (), 1e-7, 1.0, None) == T.TCM_OK
         {CHECK}
     """)
+
+
+@pytest.mark.parametrize("coef,fits", [((2.0 ** 39, 0, 0) * 2, False), ((2.0 ** -40, 0, 0) * 2, False), ((2.0 ** 60, 0, 0), True), ((2.0 ** -60, 0, 0), True),
+                                       ((0, 2.0 ** 80, 0), False), ((1, 0, 2.0 ** -81), False), ((2.0 ** 20, 0, 0) * 3, False), ((2.0 ** 15, 0, 0) * 3, True),
+                                       ((3.4445, -4.775, 2.0315) * 20, True)])
+def test_coefficients_that_leave_the_range(tmp_path, coef, fits):
+    host_util.run(tmp_path, f"""
+        for n in (20, 200):
+            st = T.tcm_orthogonalize(1, n, 300, at(1), 300, 0, at(2), 300, 0, T.TCM_F32_F32, {coef}, 0.0, 1.0, None)
+            assert st == (T.TCM_OK if {fits} else T.TCM_ERR_NOT_SUPPORTED), st
+            assert bool(launches()) == {fits}
+    """)
