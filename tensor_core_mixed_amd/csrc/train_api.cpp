@@ -112,21 +112,20 @@ int route_grad_impl(int64_t tokens, int64_t experts, int64_t topk, const void* l
     return done(launch_route_grad(t, a, stream));
 }
 
-// The largest |f| among [0, r] of f(s) = a s + b s^3 + c s^5 (in t = s^2: at the ends and where a + 3 b t + 5 c t^2 = 0)
+// The largest |f| among [0, r] of f(s) = a s + b s^3 + c s^5 (in t = s^2: at the ends and where a + 3 b t + 5 c t^2 = 0).
+// The two roots are q / (5 c) and a / q with q of one sign's sum: nothing cancels where c is next to nothing and one of
+// them lies far away.
 double largest_step(double a, double b, double c, double r) {
     const auto f = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + t * c))); };
     double most = f(r * r);
     const auto at = [&](double t) {
         if (t > 0 && t < r * r) most = std::max(most, f(t));
     };
-    if (c != 0) {
-        const double d = 9 * b * b - 20 * a * c;
-        if (d >= 0) {
-            at((-3 * b + std::sqrt(d)) / (10 * c));
-            at((-3 * b - std::sqrt(d)) / (10 * c));
-        }
-    } else if (b != 0) {
-        at(-a / (3 * b));
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0) {
+        const double q = -0.5 * (3 * b + std::copysign(std::sqrt(d), b));
+        if (c != 0) at(q / (5 * c));
+        if (q != 0) at(a / q);
     }
     return most;
 }
