@@ -106,6 +106,8 @@ struct BalanceArgs {
 };
 // a workgroup's waves in the two ways to run, and the most workgroups of the second
 constexpr int kBalanceWaves = 8, kBalanceOneWaves = 16, kBalanceGroups = 256, kBalanceOneTokens = 128;
+// a lane's tokens whose shares are added in binary32
+constexpr int kBalanceRun = 32;
 int launch_balance(int x_type, const BalanceArgs& a, void* stream);
 
 struct RouteGradArgs {

@@ -29,10 +29,16 @@
 // holds runs of experts that one load brings.  The losses' sums run over a
 // lane's tokens in registers, over a workgroup in LDS and over the workgroups
 // in a second launch, each in a fixed order; counts are integers, whose order
-// plays no part.
+// plays no part.  A lane adds the shares of 32 tokens at most in binary32 (they
+// have one sign, so a long sum's roundings can all go one way: 2200 shares of
+// 1 / 600 are off by 3e-5, 2^17 by 1.4e-3); those runs and what follows are
+// added in binary64, with one rounding to binary32 a workgroup.  The longer
+// calls have their own instance: 200000 x 384 168 to 170 us, where 16384 x 256
+// would take 0.5 us more for what it does not need.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "fp8_util.h"
 #include "lowp.h"
@@ -243,12 +249,13 @@ __device__ __forceinline__ int wave_sum(int v) {
     return v;
 }
 
-// ONE: a single workgroup does everything.  Else it leaves its partial sums.
-template <int XT, int LPT, int NPL, bool SIG, bool ONE>
+// ONE: a single workgroup does everything.  Else it leaves its partial sums.  LONG: a lane takes more than kBalanceRun
+// tokens, and adds the shares of so many to a binary64 sum.
+template <int XT, int LPT, int NPL, bool SIG, bool ONE, bool LONG>
 __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void balance_kernel(BalanceArgs a) {
     using Y = Layout<XT, LPT, NPL>;
     constexpr int W = ONE ? kBalanceOneWaves : kBalanceWaves, E = NPL * LPT, TPW = 64 / LPT;
-    __shared__ float sp[W * TPW][E];
+    __shared__ std::conditional_t<LONG, double, float> sp[W * TPW][E];
     __shared__ int hist[E], sv[W];
     __shared__ double sz[W], sd[W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane % LPT, group = wave * TPW + lane / LPT;
@@ -256,11 +263,24 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
     __syncthreads();
     float acc[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) acc[i] = 0.f;
+    for (int i = 0; i < NPL; ++i) {
+        acc[i] = 0.f;
+        if constexpr (LONG) sp[group][Y::expert(i, sub)] = 0;
+    }
     double z = 0;
-    int valid = 0;
+    int valid = 0, run = 0;
     const int64_t step = (int64_t)gridDim.x * W * TPW;
     for (int64_t t0 = (int64_t)blockIdx.x * W * TPW; t0 < a.tokens; t0 += step) {
+        if constexpr (LONG) {
+            if (run++ == kBalanceRun) {
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    sp[group][Y::expert(i, sub)] += (double)acc[i];
+                    acc[i] = 0.f;
+                }
+                run = 1;
+            }
+        }
         const int64_t t = t0 + group;
         const bool on = t < a.tokens && !(a.mask && a.mask[min(t, a.tokens - 1)] == 0);
         if (__ballot(on) == 0) continue;
@@ -299,7 +319,10 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
         }
     }
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) sp[group][Y::expert(i, sub)] = acc[i];
+    for (int i = 0; i < NPL; ++i) {
+        if constexpr (LONG) sp[group][Y::expert(i, sub)] += (double)acc[i];
+        else sp[group][Y::expert(i, sub)] = acc[i];
+    }
     z = wave_sum(z);
     valid = wave_sum(valid);
     if (lane == 0) sz[wave] = z, sv[wave] = valid;
@@ -308,14 +331,14 @@ __global__ __launch_bounds__(64 * (ONE ? kBalanceOneWaves : kBalanceWaves)) void
     for (int w = 0; w < W; ++w) z += sz[w], valid += sv[w];
     double dot = 0;
     for (int e = tid; e < a.experts; e += 64 * W) {
-        float s = 0.f;
+        double s = 0;
 #pragma unroll 8
-        for (int g = 0; g < W * TPW; ++g) s += sp[g][e];  // in the groups' order
+        for (int g = 0; g < W * TPW; ++g) s += (double)sp[g][e];  // in the groups' order
         if constexpr (ONE) {
             a.counts[e] = hist[e];
-            dot += (double)hist[e] * (double)s;
+            dot += (double)hist[e] * s;
         } else {
-            a.p[(int64_t)blockIdx.x * a.experts + e] = s;
+            a.p[(int64_t)blockIdx.x * a.experts + e] = (float)s;
             a.n[(int64_t)blockIdx.x * (a.experts + 1) + e] = hist[e];
         }
     }
@@ -395,13 +418,19 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(BalanceAr
 
 template <int XT, int LPT, int NPL>
 int balance_n(const BalanceArgs& a, hipStream_t s) {
+    const auto launch = [&](auto sig, auto one, auto lng) {
+        hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, sig(), one(), lng()>), dim3((unsigned)a.groups),
+                           dim3(64 * (one() ? kBalanceOneWaves : kBalanceWaves)), 0, s, a);
+    };
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
     if (a.groups <= 1) {
-        if (a.sigmoid) hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, true, true>), dim3(1), dim3(64 * kBalanceOneWaves), 0, s, a);
-        else hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, false, true>), dim3(1), dim3(64 * kBalanceOneWaves), 0, s, a);
+        if (a.sigmoid) launch(yes, yes, no);
+        else launch(no, yes, no);
     } else {
-        const dim3 grid((unsigned)a.groups), block(64 * kBalanceWaves);
-        if (a.sigmoid) hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, true, false>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((balance_kernel<XT, LPT, NPL, false, false>), grid, block, 0, s, a);
+        const bool lng = a.tokens > (int64_t)a.groups * kBalanceWaves * (64 / LPT) * kBalanceRun;
+        if (a.sigmoid) lng ? launch(yes, no, yes) : launch(yes, no, no);
+        else lng ? launch(no, no, yes) : launch(no, no, no);
         hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)((a.experts + kJoinExperts - 1) / kJoinExperts)),
                            dim3(64 * kJoinWaves), 0, s, a);
     }
