@@ -237,10 +237,11 @@ __device__ __forceinline__ void far_shares(float (&p)[NPL], Sum* total, const fl
     *total = token_sum<LPT>(u);
 }
 
-// (losses from sums: the choices' share of an expert is n_e / (T k))
+// (losses from sums: the choices' share of an expert is n_e / (T k); a +inf logit, whose sigmoid is 1, makes both NaN, as it
+// does the softmax's)
 __device__ __forceinline__ void store_losses(const BalanceArgs& a, double dot, double z, int valid) {
     const double t = valid > 0 ? valid : 1, k = a.topk > 0 ? a.topk : 1;
-    a.losses[0] = (float)((double)a.experts * dot / (t * k * t));
+    a.losses[0] = z != z ? __builtin_nanf("") : (float)((double)a.experts * dot / (t * k * t));
     a.losses[1] = (float)(z / t);
 }
 __device__ __forceinline__ double wave_sum(double v) { return token_sum<64>(v); }
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(BalanceAr
     const uint64_t mine = part <= 1.5 ? (uint64_t)(part * (double)(1ull << kFraction) + 0.5) : 1ull << kNans;
     const uint64_t sum = mine + __hip_atomic_fetch_add(a.arrived, mine + (1ull << kArrivals), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if ((sum >> kArrivals) != gridDim.x - 1) return;
-    const bool nan = (sum >> kNans) & 127;
+    const bool nan = ((sum >> kNans) & 127) || z != z;
     a.counts[a.experts] = valid;
     a.losses[0] = nan ? __builtin_nanf("") : (float)((double)a.experts * ((double)(sum & ((1ull << kNans) - 1)) / (double)(1ull << kFraction)));
     a.losses[1] = (float)(z / t);
