@@ -606,7 +606,9 @@ int tcm_moe_balance(int64_t tokens, int64_t experts, int64_t topk,
  *                not overlap an input.
  * (tcm_moe_route's bias moves the choice only, so it plays no part.)  A token
  * whose logits are all -inf has a row of zeros; NaN and +inf logits give NaN.
- * Limits and statuses as tcm_moe_balance.  Allocates nothing.
+ * A token's row has the same bits wherever the token lies and whatever the
+ * others hold.  Limits and statuses as tcm_moe_balance (but tokens * topk may
+ * be any number).  Allocates nothing.
  */
 int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
                        const void* logits, int64_t ldx, int dtype, float scale,

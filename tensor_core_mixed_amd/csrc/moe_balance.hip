@@ -191,7 +191,8 @@ struct Layout {
 };
 
 // Of a token: exp(x - *at), and with SIG the sigmoids and 1 minus them.  False for a token of nothing but -inf.  Where
-// every logit of the wave's tokens lies near 0 (`far`: not), one exponential serves, and no maximum is needed.
+// every logit of a token lies near 0 (`far`: not), one exponential serves, and no maximum is needed.  A wave with a far
+// token takes the long way for all, but by the same steps for the near ones, whose bits are the same anywhere.
 template <int LPT, int NPL, class Y, bool SIG>
 __device__ __forceinline__ bool scores(float (&e)[NPL], float (&s)[NPL], float (&r)[NPL], float* at, float (&x)[NPL], bool far, int experts,
                                        int sub) {
@@ -207,17 +208,23 @@ __device__ __forceinline__ bool scores(float (&e)[NPL], float (&s)[NPL], float (
         }
         return true;
     }
+    const bool near = LPT < 64 && !((__ballot(far) >> (threadIdx.x & 48)) & 0xffff);
     Y::no_pad(x, experts, sub);
     float mx = x[0];
 #pragma unroll
     for (int i = 1; i < NPL; ++i) mx = larger(mx, x[i]);
     mx = token_max<LPT>(mx);
-    const bool live = !(mx == -INFINITY);
-    *at = live ? mx : 0.f;
+    const bool live = near || !(mx == -INFINITY);
+    *at = live && !near ? mx : 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         e[i] = exp_neg(x[i] - *at);
-        if constexpr (SIG) s[i] = sigmoid(x[i], &r[i]);
+        if constexpr (SIG) {
+            s[i] = sigmoid(x[i], &r[i]);
+            const float y = inverse(1.f + e[i]);
+            r[i] = near ? y : r[i];
+            s[i] = near ? e[i] * y : s[i];
+        }
     }
     return live;
 }
