@@ -640,16 +640,25 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
  *                before the last step, or b s + c s^2 past 2^79 or below 2^-79,
  *                the call is refused (TCM_ERR_NOT_SUPPORTED).
  *   eps          >= 0; above 0 it keeps a matrix of zeros one of zeros.
- * Products run on the matrix cores in two binary16 parts of each value, which
- * keep 22 bits, and add in binary32; scales from the coefficients keep them
- * within range.  The result is as exact as with binary32 products.  The sum of
- * squares is a binary64 one.  A NaN makes its entry NaN, and so does an
- * infinity (with no steps its own value only, and zeros of the others).  Any
- * alignment.  rows and cols up to 2^20 - 32 (else TCM_ERR_NOT_SUPPORTED).
- * Returns as tcm_gemm; the workspace rules are tcm_gemm's (it holds G five
- * times in f32's size, for as many entries as 2 GiB take, one at least;
- * entries with one side up to 64 and the other up to 256, or both up to 128,
- * use none in calls of up to 16 steps).
+ * Products run on the matrix cores in two binary16 parts of each value and add
+ * in binary32.  The parts' scale is one for a whole matrix and comes from the
+ * coefficients, so that nothing leaves their range: a value of X, of X X^T and
+ * of what multiplies X is held to 2^-23 of itself or to 2^-38 of the bound on
+ * their singular values (X's is 1 at first), whichever is more.  Where G's
+ * rows and columns are within 2^12 of one another in size, the error of the
+ * result is at most four times that of binary32 products, or 2^-20.  Parts of G
+ * further below its norm keep fewer bits once the steps raise them: rows at
+ * 2^-16 of the others', brought to 1, are off by 1e-5 of themselves, at 2^-20 by
+ * 2e-4 (binary32: 3e-7), and values below 2^-39 of the norm count as zeros.  An
+ * eps above the norm takes X there as well.  Results below 2^-100 may lose
+ * bits.  The sum of squares is a binary64 one.  A NaN makes its entry NaN, and
+ * so does an infinity (with no steps its own value only, and zeros of the
+ * others).  Any alignment.  rows and cols up to 2^20 - 32 (else
+ * TCM_ERR_NOT_SUPPORTED).
+ * Returns as tcm_gemm; the workspace rules are tcm_gemm's (it holds G, both
+ * sides rounded up to 32, five times in f32's size at most, for as many
+ * entries as 2 GiB take, one at least; entries with one side up to 64 and the
+ * other up to 256, or both up to 128, use none in calls of up to 16 steps).
  */
 int tcm_orthogonalize(int64_t batch, int64_t rows, int64_t cols,
                       const void* G, int64_t ldg, int64_t stride_g,

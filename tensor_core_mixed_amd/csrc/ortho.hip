@@ -13,8 +13,15 @@
 // rate.  The exponents e come from bounds: singular values of X lie below 1
 // at first, then below the largest |a s + b s^3 + c s^5| there, and entries
 // below singular values; so nothing passes binary16's range whatever G and
-// the coefficients are, and entries down to 2^-28 of the bound keep 11 bits
-// or more.
+// the coefficients are.
+//
+// One exponent a matrix costs bits where its parts differ in size: lower parts
+// end at 2^-24, so a value is held to 2^-38 of the bound at best, and those
+// below 2^-39 are zeros.  Rows of 2^-p of the others', brought to 1 by steps
+// (1.5, -0.5, 0), are off by 5e-7 of themselves at p = 12, 8e-6 at 16, 1.4e-4
+// at 20 and 2e-3 at 24, where binary32 stays at 2e-7; five of Muon's steps of
+// such a matrix at p = 20 are off by 1.7e-6 of the whole.  (Three bfloat16
+// parts have binary32's range and bits, in six instructions.)
 //
 // Parts lie as the main loop of pair_tile.h takes them: rows of 128-byte
 // pieces, 32 upper parts then their 32 lower ones; rows end in zeros up to a
