@@ -576,9 +576,14 @@ int tcm_gemm_mxfp4(int64_t M, int64_t N, int64_t K,
  * tcm_moe_route_grad's.  experts <= 1024, topk <= 64 and tokens * topk < 2^31
  * (else TCM_ERR_NOT_SUPPORTED), topk <= experts, tokens < 2^31.  A token whose
  * logits are all -inf adds nothing to the losses; NaN and +inf logits make
- * them NaN.  losses[0] is held to 2^-34 (it is about 1 where the load is even),
- * losses[1] relative to itself.  The same call gives the same bits.  Returns as tcm_gemm; the
- * workspace rules are tcm_gemm's (calls of up to 128 tokens use none).
+ * them NaN.  With r the size of the largest logit plus the range of them all
+ * (-inf apart), losses[0] is off by (r + 110) 2^-23 of itself at most, and by
+ * 2^-34 more in calls of more than 128 tokens (it is about 1 where the load is
+ * even, and never that small where the choices follow the scores); a token's
+ * log is off by (r + 30) 2^-23 and as many of itself, so a losses[1] near 0 is
+ * not exact relative to itself.  The same call gives the same bits.  Returns as
+ * tcm_gemm; the workspace rules are tcm_gemm's (calls of up to 128 tokens use
+ * none).
  */
 int tcm_moe_balance(int64_t tokens, int64_t experts, int64_t topk,
                     const void* logits, int64_t ldx, int dtype,
@@ -646,8 +651,8 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
  * of what multiplies X is held to 2^-23 of itself or to 2^-38 of the bound on
  * their singular values (X's is 1 at first), whichever is more.  Where G's
  * rows and columns are within 2^12 of one another in size, the error of the
- * result is at most four times that of binary32 products, or 2^-20.  Parts of G
- * further below its norm keep fewer bits once the steps raise them: rows at
+ * result is at most four times that of binary32 products, or 2^-20 (2^-16 for
+ * sides under 8).  Parts of G further below its norm keep fewer bits once the steps raise them: rows at
  * 2^-16 of the others', brought to 1, are off by 1e-5 of themselves, at 2^-20 by
  * 2e-4 (binary32: 3e-7), and values below 2^-39 of the norm count as zeros.  An
  * eps above the norm takes X there as well.  Results below 2^-100 may lose
