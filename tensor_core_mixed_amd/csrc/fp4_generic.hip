@@ -6,7 +6,9 @@
 // a 64 x 64 tile a workgroup, 4 x 4 outputs a thread, operands decoded to
 // binary32 on their way to LDS one byte at a time.  P_b is a multiple of 1/4
 // below 2^11: exact.  The two scales are added as exponents, so only the
-// scaled block leaves binary32's range where it does.
+// scaled block leaves binary32's range where it does.  It multiplies on the vector
+// ALU (37 x 5120 x 8192: 857 us, 12 on the tiles): operands at 16 bytes are what
+// is meant to be fast.
 #include <hip/hip_runtime.h>
 
 #include "fp8_util.h"

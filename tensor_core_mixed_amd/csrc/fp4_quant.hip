@@ -22,11 +22,15 @@
 // through LDS to be stored 64 bytes of a column at a time.  Row kernel: row
 // blocks as they lie need no tile; short matrices fill more of the chip.
 //
-// Memory bounds all of them: 8003 x 8192 bf16 to both outputs 62 us from HBM
-// (201 MB, 3.2 TB/s; 47 with x in the caches), back from rows 25 (166 MB) and
-// from columns with odd pitches 38, whose 16-byte stores lie across lines.
-// 16 x 4096: 2.4 us.  A tile of 256 x 256 by 1024 threads took 52 us for 48
-// (binary32 109 for 71); for odd pitches stores aligned row by row 82 for 37,
+// Row blocks run at a copy's rate: 8003 x 8192 bf16 36 us (166 MB, 4.7 TB/s),
+// binary32 63 (297 MB); back from rows 25.  Both outputs do not: 64 us from
+// HBM (201 MB, 3.1 TB/s; 48 with x in the caches), binary32 102 (333 MB).  A
+// tile is loaded, encoded and stored by 3.7 waves a SIMD with none of the next
+// one in flight: waves wait for memory in 48% of their cycles and for a turn
+// to issue in 39%, the vector ALU is busy in a third.  Back from columns with
+// odd pitches 37, whose 16-byte stores lie across lines.  16 x 4096: 2.4 us.
+// A tile of 256 x 256 by 1024 threads took 52 us for 48 (binary32 109 for 71,
+// x in the caches); for odd pitches stores aligned row by row 82 for 37,
 // workgroups of two or four longer pieces of rows 44.
 #include <hip/hip_runtime.h>
 

@@ -6,12 +6,13 @@
 // on the main loop of pair_tile.h: the matrix instruction's block scales are
 // the format's, so a K-step is nothing but copies, LDS reads and products.
 //
-// 8192^3 takes 254 to 264 us (4.2 PFLOP/s) on 256 x 256 tiles: the products
+// 8192^3 takes 254 to 268 us (4.2 PFLOP/s) on 256 x 256 tiles: the products
 // alone 157, the copies alone 196, all but the copies 173, all but the scales'
 // copies 250, all but the LDS reads 232; so the copies bound it, and with them
 // the two stages that fit (four of 64-byte rows, half lines: 276).  4096 x
-// 4096 x 5003 with binary32 C 60 us (2.8 PFLOP/s), one round of 256 tiles.
-// 37 x 5120 x 8192 on 64 x 128 tiles: 8.8 us and 2.8 for the sum.  Eight waves
+// 4096 x 5003 with binary32 C 62 us (2.7 PFLOP/s), one round of 256 tiles.
+// 37 x 5120 x 8192 on 64 x 128 tiles: 10 us and 4.0 for the sum (9 and 2.8 at
+// least), 160 workgroups on 256 CUs.  Eight waves
 // and three stages on 128 x 128 tiles gain where a tile is all a CU has
 // (300 x 5120 x 8192 22.5 us for 28.3, where 64 x 128 tiles take 17.1) and
 // lose where it has more (4096^3 58 for 47).

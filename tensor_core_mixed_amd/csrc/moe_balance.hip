@@ -23,9 +23,11 @@
 //
 // Sixteen lanes take a token of up to 256 experts, so a sum over them is four
 // steps on the vector ALU for four tokens at once (a wave a token: gradient
-// of 16384 x 256 28.5 us, now 12.6; losses' first launch 15.4, now 7.8; 17.8
-// and 8.9 MB, so instructions bound both: an exponential or two a value, the
-// sums, binary64); a wave takes one of more.  A lane
+// of 16384 x 256 28.5 us, now 12.8; losses' first launch 15.4, now 7.9); a wave
+// takes one of more.  17.8 and 8.9 MB are not what bounds them: the vector ALU
+// issues in 57% and 49% of the cycles (an exponential or two a value, the sums,
+// binary64), with 1.9 waves a SIMD (231 and 136 registers; 256 workgroups of
+// eight waves), which wait for their loads and row sums half of the time.  A lane
 // holds runs of experts that one load brings.  The losses' sums run over a
 // lane's tokens in registers, over a workgroup in LDS and over the workgroups
 // in a second launch, each in a fixed order; counts are integers, whose order

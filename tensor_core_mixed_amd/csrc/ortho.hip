@@ -40,11 +40,12 @@
 // ranges, one a workgroup, and a second launch adds the partial tiles in order
 // and finishes them.
 //
-// Five steps of 4096 x 1024 take 346 to 357 us: 209 GFLOP of binary16, 144 us
+// Five steps of 4096 x 1024 take 345 to 364 us: 209 GFLOP of binary16, 144 us
 // at the rate that a library product of 8192^3 reaches (1458 TFLOP/s), the
 // rest being the launches' fill, the way out of 48 MB of X a step and copies
-// that arrive late.  Eight 768 x 2048: 665 us (floor 336), 4096 x 4096: 3640
-// (2830).  128 x 128 tiles are taken by eight waves with copies two steps
+// that arrive late (matrix cores busy in 48 and 45% of S's and X's cycles, in
+// 23% of T's, which has 136 workgroups of four waves).  Eight 768 x 2048: 665 to 690 us
+// (floor 336), 4096 x 4096: 3640 (2830).  128 x 128 tiles are taken by eight waves with copies two steps
 // ahead (S of 4096 x 1024 19 us and X 31; by two groups of four waves, one
 // step ahead, 21 and 36), 64 x 64 by two groups, two steps ahead (512 x 512
 // 154 us in all; by four groups, one step ahead, 170).  Shorter sides up to
