@@ -652,14 +652,14 @@ int tcm_moe_route_grad(int64_t tokens, int64_t experts, int64_t topk,
  * their singular values (X's is 1 at first), whichever is more.  Where G's
  * rows and columns are within 2^12 of one another in size, the error of the
  * result is at most four times that of binary32 products, or 2^-20 (2^-16 for
- * sides under 8).  Parts of G further below its norm keep fewer bits once the steps raise them: rows at
- * 2^-16 of the others', brought to 1, are off by 1e-5 of themselves, at 2^-20 by
- * 2e-4 (binary32: 3e-7), and values below 2^-39 of the norm count as zeros.  An
- * eps above the norm takes X there as well.  Results below 2^-100 may lose
- * bits.  The sum of squares is a binary64 one.  A NaN makes its entry NaN, and
- * so does an infinity (with no steps its own value only, and zeros of the
- * others).  Any alignment.  rows and cols up to 2^20 - 32 (else
- * TCM_ERR_NOT_SUPPORTED).
+ * sides under 8).  Parts of G further below its norm keep fewer bits once the
+ * steps raise them: rows at 2^-16 of the others', brought to 1, are off by 1e-5
+ * of themselves, at 2^-20 by 2e-4 (binary32: 3e-7), and values below 2^-39 of
+ * the norm count as zeros.  An eps above the norm takes X there as well.
+ * Results below 2^-100 may lose bits.  The sum of squares is a binary64 one.  A
+ * NaN makes its entry NaN, and so does an infinity (with no steps its own value
+ * only, and zeros of the others).  Any alignment.  rows and cols up to 2^20 - 32
+ * (else TCM_ERR_NOT_SUPPORTED).
  * Returns as tcm_gemm; the workspace rules are tcm_gemm's (it holds G, both
  * sides rounded up to 32, five times in f32's size at most, for as many
  * entries as 2 GiB take, one at least; entries with one side up to 64 and the
